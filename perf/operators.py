@@ -211,12 +211,17 @@ def _norm(st):
         return q.view(m, k), st["sf"].view(torch.float8_e8m0fnu), res
     kb = -(-k // group)
     a = torch.nn.functional.pad(y, (0, kb * group - k)).view(m, kb, group)
-    s = a.abs().amax(2) / QMAX[kind]
+    s = _over_q(a.abs().amax(2), kind)
     c = torch.where(s[..., None] > 0, a / s[..., None], 0.0)
     c = c.round().clamp(-128, 127).to(torch.int8) if kind == "int8" else c.clamp(-448, 448).to(FP8)
     q = c.view(torch.uint8).view(m, kb * group)[:, :k].contiguous()
     s = s.t().contiguous()
     return (q.view(FP8) if kind == "fp8" else _values(q.view(torch.int8), s, group)), s, res
+
+
+def _over_q(amax, kind):
+    """amax / Q, one division (by a tensor: torch multiplies by the reciprocal of a number)."""
+    return amax / torch.full_like(amax, QMAX[kind])
 
 
 def _values(c, s, group):
@@ -274,7 +279,7 @@ def _append(st):
             heads = torch.arange(x.shape[1], device=dev)
             before = codes[where[:, None, None], heads[None, :, None], slot[:, None]]
             s0 = torch.where(was.any(1)[:, None], scales[where, :, sub], 0.0)
-            s1 = torch.maximum(s0, fresh.abs().amax((2, 3)) / QMAX[kind])[..., None, None]
+            s1 = torch.maximum(s0, _over_q(fresh.abs().amax((2, 3)), kind))[..., None, None]
             stood = before.view(torch.int8 if kind == "int8" else FP8).float() * s0[..., None, None]
             c = torch.where(s1 > 0, torch.where(is_new[:, None, :, None], fresh, stood) / s1, 0.0)
             c = c.round().clamp(-128, 127).to(torch.int8) if kind == "int8" else c.clamp(-448, 448).to(FP8)
