@@ -10,12 +10,15 @@ Layouts (see include/bq.h):
   activation scales float32 [ceil(K/group_k), M]   (K-block-major)
   weight codes      uint8 [N, K];  weight scales float32 [ceil(N/bn), ceil(K/bk)]
   outputs           bfloat16 [M, N]
+  cache of keys and values: see KvCache
 """
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -25,6 +28,9 @@ FP8_E4M3 = 1
 PATH_AUTO, PATH_SIMT, PATH_TCGEN05, PATH_DECODE, PATH_TCGEN05_1CTA, PATH_TCGEN05_PAIR = \
     0, 1, 2, 3, 4, 5
 
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_YARN = range(4)
+
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_ALIGNMENT, ERR_WORKSPACE, ERR_CUDA, \
     ERR_DEVICE_TIMEOUT = range(7)
 
@@ -32,6 +38,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libbq.so")
 
 _P, _I64, _INT, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
 _SZP = ctypes.POINTER(ctypes.c_size_t)
+_F32, _F64 = ctypes.c_float, ctypes.c_double
 
 # name -> (restype, argtypes); mirrors include/bq.h one to one.
 DECLS = {
@@ -80,6 +87,21 @@ DECLS = {
     "bq_mx_linear": (_INT, [_P, _I64, _I64, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _P, _SZ,
                             _P]),
     "bq_moe_combine": (_INT, [_P, _I64, _P, _P, _I64, _I64, _I64, _P, _I64, _P]),
+    "bq_rmsnorm_quant": (_INT, [_P, _I64, _P, _I64, _P, _F32, _F32, _I64, _I64, _I64, _INT, _P,
+                                _I64, _P, _P, _I64, _P, _I64, _P]),
+    "bq_mx_rmsnorm_quant": (_INT, [_P, _I64, _P, _I64, _P, _F32, _F32, _I64, _I64, _P, _I64, _P,
+                                   _P, _I64, _P, _I64, _P]),
+    "bq_rope_frequencies": (_INT, [_I64, _F64, _INT, _F64, _I64, _F64, _F64,
+                                   ctypes.POINTER(_F64), ctypes.POINTER(_F32)]),
+    "bq_rope": (_INT, [_P, _I64, _I64, _P, _P, _I64, _I64, _I64, _I64, _INT, _F32, _P, _I64,
+                       _I64, _P]),
+    "bq_kv_append": (_INT, [_P, _I64, _I64, _P, _I64, _I64, _P, _P, _P, _I64, _I64, _I64, _I64,
+                            _I64, _I64, _I64, _I64, _I64, _INT, _P, _P, _P, _P, _P]),
+    "bq_kv_attention_workspace_size": (_INT, [_I64, _I64, _I64, _I64, _I64, _I64, _I64, _I64,
+                                              _I64, _SZP]),
+    "bq_kv_attention": (_INT, [_P, _I64, _I64, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64,
+                               _I64, _I64, _I64, _P, _P, _P, _P, _I64, _I64, _I64, _INT, _F32,
+                               _INT, _I64, _P, _I64, _I64, _P, _P, _SZ, _P]),
 }
 
 _lib = None
@@ -513,4 +535,274 @@ def moe_combine(y, inv_perm, topk_w, out=None):
     _check(lib().bq_moe_combine(_cuda(y, "y"), _ld(y), _cuda(inv_perm, "inv_perm"),
                                 _cuda(topk_w, "topk_w"), T, topk, H, _cuda(out, "out"),
                                 _ld(out), _P(_stream(y.device))))
+    return out
+
+
+# ---- between two linears: norm, rotary positions, cache, attention ----------
+
+def _need(cond: bool, msg: str):
+    if not cond:
+        raise ValueError(msg)
+
+
+class _on:
+    """The device of a call's tensors as the current one, for the launch."""
+
+    def __init__(self, dev: torch.device):
+        self.idx = dev.index
+
+    def __enter__(self):
+        self.prev = torch.cuda.current_device()
+        if self.prev != self.idx:
+            torch.cuda.set_device(self.idx)
+
+    def __exit__(self, *exc):
+        if self.prev != self.idx:
+            torch.cuda.set_device(self.prev)
+
+
+def _same_device(dev, **tensors):
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        _cuda(t, name)
+        _need(t.device == dev, f"{name} must be on {dev}, not {t.device}")
+
+
+def _matrix(t, name, dtype, M, K):
+    _need(t.dtype == dtype and t.dim() == 2 and t.shape[0] == M and t.shape[1] == K,
+          f"{name} must be {dtype} [{M}, {K}]")
+    _need(t.stride(1) == 1 or K <= 1, f"{name} must have unit column stride")
+    _need(t.stride(0) >= K or M <= 1, f"{name}: rows overlap")
+
+
+def _row_stride(t, K):
+    return max(t.stride(0), K)
+
+
+def _rmsnorm(x, weight, eps, residual, weight_offset, want_h, q, scales, res_out, h, call):
+    _cuda(x, "x")
+    _need(x.dim() == 2, "x must be bfloat16 [M, K]")
+    M, K = x.shape
+    dev, bf16 = x.device, torch.bfloat16
+    if q is None:
+        q = torch.empty(M, K, dtype=torch.uint8, device=dev)
+    if residual is not None and res_out is None:
+        res_out = torch.empty(M, K, dtype=bf16, device=dev)
+    if want_h and h is None:
+        h = torch.empty(M, K, dtype=bf16, device=dev)
+    _same_device(dev, weight=weight, residual=residual, q=q, scales=scales, res_out=res_out, h=h)
+    _need(weight.dtype == bf16 and weight.shape == (K,) and weight.is_contiguous(),
+          f"weight must be bfloat16 [{K}], dense")
+    _matrix(x, "x", bf16, M, K)
+    _matrix(q, "q", torch.uint8, M, K)
+    for t, name in ((residual, "residual"), (res_out, "res_out"), (h, "h")):
+        if t is not None:
+            _matrix(t, name, bf16, M, K)
+    with _on(dev):
+        _check(call(
+            x.data_ptr(), _row_stride(x, K), _opt(residual, "residual"),
+            K if residual is None else _row_stride(residual, K), weight.data_ptr(),
+            weight_offset, eps, M, K, q.data_ptr(), _row_stride(q, K), scales.data_ptr(),
+            _opt(res_out, "res_out"), K if res_out is None else _row_stride(res_out, K),
+            _opt(h, "h"), K if h is None else _row_stride(h, K), _stream(dev)))
+    return (q, scales) + ((res_out,) if res_out is not None else ()) + \
+        ((h,) if h is not None else ())
+
+
+def rmsnorm_quant(x, weight, eps=1e-6, residual=None, group_k=128, dtype=INT8, weight_offset=0.0,
+                  want_h=False, q=None, s=None, res_out=None, h=None):
+    """RMS norm of bf16(x + residual), quantised 1 x group_k for the next linear.
+
+    x, residual: bf16 [M, K]; weight: bf16 [K].  Returns (q [M, K], s [Kb, M]),
+    then res_out = bf16(x + residual) if there is a residual (or res_out is
+    given), then h = bf16(y) if want_h.  res_out may be residual or x."""
+    M, K = x.shape
+    _need(group_k >= 1, "group_k must be >= 1")
+    if s is None:
+        s = torch.empty(cdiv(K, group_k), M, dtype=torch.float32, device=x.device)
+    _need(s.dtype == torch.float32 and s.shape == (cdiv(K, group_k), M) and s.is_contiguous(),
+          f"s must be float32 [{cdiv(K, group_k)}, {M}], dense")
+
+    def call(x_, ldx, r_, ldr, w_, off, eps_, M_, K_, q_, ldq, s_, ro, ldro, h_, ldh, st):
+        return lib().bq_rmsnorm_quant(x_, ldx, r_, ldr, w_, off, eps_, M_, K_, group_k, dtype, q_,
+                                      ldq, s_, ro, ldro, h_, ldh, st)
+
+    return _rmsnorm(x, weight, eps, residual, weight_offset, want_h, q, s, res_out, h, call)
+
+
+def mx_rmsnorm_quant(x, weight, eps=1e-6, residual=None, weight_offset=0.0, want_h=False, q=None,
+                     sf=None, res_out=None, h=None):
+    """rmsnorm_quant with MXFP8 codes and scale atoms, for mx_gemm."""
+    M, K = x.shape
+    n = mx_scale_bytes(M, K)
+    if sf is None:
+        sf = torch.empty(n, dtype=torch.uint8, device=x.device)
+    _need(sf.dtype == torch.uint8 and sf.numel() >= n and sf.is_contiguous(),
+          f"sf must be uint8, dense, of at least {n} bytes")
+    return _rmsnorm(x, weight, eps, residual, weight_offset, want_h, q, sf, res_out, h,
+                    lib().bq_mx_rmsnorm_quant)
+
+
+def rope_frequencies(rot_dim, base=10000.0, scaling=ROPE_PLAIN, factor=1.0, orig_max_pos=0,
+                     beta_fast=32.0, beta_slow=1.0, device="cuda"):
+    """(turns, mscale) for rope(): float64 [rot_dim/2] turns per position on
+    `device`, and the factor on the rotated pairs (1 but for ROPE_YARN)."""
+    _need(rot_dim >= 0, "rot_dim must be >= 0")
+    host = torch.empty(rot_dim // 2, dtype=torch.float64)
+    ms = _F32(0.0)
+    _check(lib().bq_rope_frequencies(
+        rot_dim, base, scaling, factor, orig_max_pos, beta_fast, beta_slow,
+        ctypes.cast(host.data_ptr(), ctypes.POINTER(_F64)), ctypes.byref(ms)))
+    return host.to(device), ms.value
+
+
+def _heads(t, name, T, H, D):
+    """Token and head strides of a bf16 [T, H, D] tensor with unit last stride."""
+    _need(t.dtype == torch.bfloat16 and t.dim() == 3 and t.shape[0] == T and t.shape[1] == H and
+          t.shape[2] == D, f"{name} must be bfloat16 [{T}, {H}, {D}]")
+    st = t.stride()
+    _need(st[2] == 1 or D <= 1, f"{name} must have unit stride in its last dimension")
+    return st[0], st[1]
+
+
+def rope(x, positions, freqs, layout=ROPE_HALF, mscale=1.0, out=None):
+    """Rotary positions on bf16 x [T, H, D] (any token and head strides): the
+    first 2 * len(freqs) dimensions of each head are turned, the rest copied.
+    positions: int32 [T]; freqs, mscale: from rope_frequencies.  out may be x."""
+    _cuda(x, "x")
+    _need(x.dim() == 3, "x must be bfloat16 [T, H, D]")
+    T, H, D = x.shape
+    if out is None:
+        out = torch.empty(T, H, D, dtype=torch.bfloat16, device=x.device)
+    _same_device(x.device, positions=positions, freqs=freqs, out=out)
+    _need(positions.dtype == torch.int32 and positions.shape == (T,) and
+          (positions.stride(0) == 1 or T <= 1), f"positions must be int32 [{T}], dense")
+    _need(freqs.dtype == torch.float64 and freqs.dim() == 1 and freqs.is_contiguous(),
+          "freqs must be float64 [rot_dim / 2], dense")
+    xt, xh = _heads(x, "x", T, H, D)
+    ot, oh = _heads(out, "out", T, H, D)
+    with _on(x.device):
+        _check(lib().bq_rope(x.data_ptr(), xt, xh, positions.data_ptr(), freqs.data_ptr(), T, H,
+                             D, 2 * freqs.shape[0], layout, mscale, out.data_ptr(), ot, oh,
+                             _stream(x.device)))
+    return out
+
+
+class KvCache(NamedTuple):
+    """A paged 8-bit cache: codes uint8 [n_pages, Hkv, page_size, D] and scales
+    float32 [n_pages, Hkv, page_size / block_t] of keys and values, all dense."""
+    k: torch.Tensor
+    v: torch.Tensor
+    ks: torch.Tensor
+    vs: torch.Tensor
+    dtype: int = INT8
+
+
+def kv_cache(n_pages, n_heads, page_size, head_dim, block_t=16, dtype=INT8, device="cuda"):
+    """An empty cache."""
+    _need(block_t >= 1 and page_size % block_t == 0, "block_t must divide page_size")
+    codes = [torch.zeros(n_pages, n_heads, page_size, head_dim, dtype=torch.uint8, device=device)
+             for _ in range(2)]
+    scales = [torch.zeros(n_pages, n_heads, page_size // block_t, dtype=torch.float32,
+                          device=device) for _ in range(2)]
+    return KvCache(*codes, *scales, dtype)
+
+
+def _cache_args(cache: KvCache, dev):
+    k, v, ks, vs, dtype = cache
+    _same_device(dev, k=k, v=v, ks=ks, vs=vs)
+    _need(k.dtype == torch.uint8 and v.dtype == torch.uint8 and k.dim() == 4 and
+          v.shape == k.shape and k.is_contiguous() and v.is_contiguous(),
+          "cache codes must be uint8 [n_pages, Hkv, page_size, D], dense and alike")
+    P, H, page, D = k.shape
+    _need(ks.dtype == torch.float32 and vs.dtype == torch.float32 and ks.dim() == 3 and
+          vs.shape == ks.shape and ks.shape[0] == P and ks.shape[1] == H and
+          ks.is_contiguous() and vs.is_contiguous(),
+          "cache scales must be float32 [n_pages, Hkv, page_size / block_t], dense and alike")
+    nb = ks.shape[2]
+    _need(page >= 1 and nb >= 1 and page % nb == 0, "block_t must divide page_size")
+    return P, H, page, D, page // nb
+
+
+def _batch_args(seq_offsets, kv_lens, page_table, dev):
+    _same_device(dev, seq_offsets=seq_offsets, kv_lens=kv_lens, page_table=page_table)
+    B = kv_lens.shape[0] if kv_lens.dim() == 1 else -1
+    _need(B >= 0 and kv_lens.dtype == torch.int32 and kv_lens.is_contiguous(),
+          "kv_lens must be int32 [B], dense")
+    _need(seq_offsets.dtype == torch.int32 and seq_offsets.shape == (B + 1,) and
+          seq_offsets.is_contiguous(), f"seq_offsets must be int32 [{B + 1}], dense")
+    _need(page_table.dtype == torch.int32 and page_table.dim() == 2 and
+          page_table.shape[0] == B, f"page_table must be int32 [{B}, pages]")
+    cols = page_table.shape[1]
+    _need(page_table.stride(1) == 1 or cols <= 1, "page_table must have unit column stride")
+    _need(page_table.stride(0) >= 0, "page_table: negative stride")
+    return B, max(page_table.stride(0), cols) if B > 1 else cols, cols
+
+
+def kv_append(cache: KvCache, k, v, seq_offsets, kv_lens, page_table):
+    """Quantise the new tokens' keys and values, bf16 [T, Hkv, D] (any token and
+    head strides), into the cache.  Rows seq_offsets[b] .. seq_offsets[b+1] are
+    the last tokens of sequence b, whose length with them is kv_lens[b];
+    page_table int32 [B, pages].  Lengths and pages are read on the device."""
+    _cuda(k, "k")
+    dev = k.device
+    P, H, page, D, bt = _cache_args(cache, dev)
+    B, ld, cols = _batch_args(seq_offsets, kv_lens, page_table, dev)
+    _same_device(dev, v=v)
+    T = k.shape[0]
+    kt, kh = _heads(k, "k", T, H, D)
+    vt, vh = _heads(v, "v", T, H, D)
+    with _on(dev):
+        _check(lib().bq_kv_append(
+            k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, seq_offsets.data_ptr(),
+            kv_lens.data_ptr(), page_table.data_ptr(), ld, cols, B, T, H, D, P, page, bt,
+            cache.dtype, cache.k.data_ptr(), cache.v.data_ptr(), cache.ks.data_ptr(),
+            cache.vs.data_ptr(), _stream(dev)))
+
+
+def kv_attention_workspace_size(B, T, Hq, Hkv, D, max_q_len, max_kv_len, page_size,
+                                block_t) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().bq_kv_attention_workspace_size(B, T, Hq, Hkv, D, max_q_len, max_kv_len,
+                                                page_size, block_t, ctypes.byref(n)))
+    return n.value
+
+
+def kv_attention(q, cache: KvCache, seq_offsets, kv_lens, page_table, max_q_len, max_kv_len,
+                 scale=None, causal=True, window=0, out=None, lse=None, ws=None):
+    """Attention of bf16 queries q [T, Hq, D] over the cache (see kv_append for
+    the batch) -> bf16 [T, Hq, D].  max_q_len, max_kv_len: bounds on the rows
+    and the length of every sequence.  scale: 1 / sqrt(D) by default; window: keys
+    a causal row sees, 0 for all.  lse: float32 [T, Hq] to fill, or None.
+    Rows at and behind seq_offsets[B] are left as they are.  Without ws, the
+    workspace is allocated for the call."""
+    _cuda(q, "q")
+    dev = q.device
+    P, H, page, D, bt = _cache_args(cache, dev)
+    B, ld, cols = _batch_args(seq_offsets, kv_lens, page_table, dev)
+    _need(q.dim() == 3, "q must be bfloat16 [T, Hq, D]")
+    T, Hq = q.shape[0], q.shape[1]
+    qt, qh = _heads(q, "q", T, Hq, D)
+    if out is None:
+        out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=dev)
+    ot, oh = _heads(out, "out", T, Hq, D)
+    _same_device(dev, out=out, lse=lse, ws=ws)
+    if lse is not None:
+        _need(lse.dtype == torch.float32 and lse.shape == (T, Hq) and lse.is_contiguous(),
+              f"lse must be float32 [{T}, {Hq}], dense")
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    with _on(dev):
+        if ws is None:
+            n = kv_attention_workspace_size(B, T, Hq, H, D, max_q_len, max_kv_len, page, bt)
+            if n:
+                ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        _check(lib().bq_kv_attention(
+            q.data_ptr(), qt, qh, seq_offsets.data_ptr(), kv_lens.data_ptr(),
+            page_table.data_ptr(), ld, cols, B, T, Hq, H, D, max_q_len, max_kv_len,
+            cache.k.data_ptr(), cache.v.data_ptr(), cache.ks.data_ptr(), cache.vs.data_ptr(), P,
+            page, bt, cache.dtype, scale, int(causal), window, out.data_ptr(), ot, oh,
+            None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(),
+            0 if ws is None else ws.numel() * ws.element_size(), _stream(dev)))
     return out

@@ -5,6 +5,7 @@
 // dimensional block size, dynamic activations, int8-serialised checkpoint;
 // section 3: tensor-parallel block alignment), then chooses a kernel family.
 #include <algorithm>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -17,6 +18,7 @@
 #include "gemm_mx.h"
 #include "gemm_paths.h"
 #include "gemm_tc.h"
+#include "layer_ops.h"
 
 namespace {
 
@@ -750,6 +752,243 @@ bq_status bq_moe_combine(const void* y, int64_t ldy, const int32_t* inv_perm,
   BQ_CHECK_CUDA(bq::launch_moe_combine(y, ldy, inv_perm, topk_w, T, topk, H, out, ldo,
                                        as_stream(stream)),
                 "moe_combine launch");
+  return ok();
+}
+
+// ---------------- between two linears ----------------
+
+static bq_status rmsnorm_impl(const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                              const void* weight, float weight_offset, float eps, int64_t M,
+                              int64_t K, int64_t group_k, int dtype, void* q, int64_t ldq,
+                              float* s, void* sf, void* res_out, int64_t ldro, void* h_out,
+                              int64_t ldh, void* stream) {
+  BQ_CHECK_ARG(M >= 0 && K >= 0, "M and K must be >= 0");
+  BQ_CHECK_ARG(ldx >= K && ldq >= K && (!residual || ldr >= K) && (!res_out || ldro >= K) &&
+                   (!h_out || ldh >= K),
+               "leading dimensions must be >= K");
+  BQ_CHECK_ARG(eps >= 0.0f && std::isfinite(eps) && std::isfinite(weight_offset),
+               "eps must be finite and >= 0, weight_offset finite");
+  if (K > bq::kNormMaxK)
+    return fail(BQ_ERR_UNSUPPORTED, "K = %lld exceeds the norm's widest row, %lld", (long long)K,
+                (long long)bq::kNormMaxK);
+  if (M == 0 || K == 0) return ok();
+  BQ_CHECK_ARG(x && weight && q && (s || sf), "x, weight, q and the scales must not be NULL");
+  BQ_CHECK_ARG(res_out == nullptr || ((res_out != x || ldro == ldx) &&
+                                      (res_out != residual || ldro == ldr)),
+               "res_out in place needs the same row stride");
+  bq::NormArgs a{};
+  a.x = static_cast<const uint16_t*>(x); a.ldx = ldx;
+  a.res = static_cast<const uint16_t*>(residual); a.ldr = ldr;
+  a.w = static_cast<const uint16_t*>(weight); a.w_off = weight_offset; a.eps = eps;
+  a.M = M; a.K = K; a.group = std::min(group_k, K); a.dtype = dtype;
+  a.q = static_cast<uint8_t*>(q); a.ldq = ldq; a.s = s; a.sf = static_cast<uint8_t*>(sf);
+  a.res_out = static_cast<uint16_t*>(res_out); a.ldro = ldro;
+  a.h = static_cast<uint16_t*>(h_out); a.ldh = ldh;
+  BQ_CHECK_CUDA(bq::launch_rmsnorm_quant(a, as_stream(stream)), "rmsnorm_quant launch");
+  return ok();
+}
+
+bq_status bq_rmsnorm_quant(const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                           const void* weight, float weight_offset, float eps, int64_t M,
+                           int64_t K, int64_t group_k, int dtype, void* q, int64_t ldq, float* s,
+                           void* res_out, int64_t ldro, void* h_out, int64_t ldh, void* stream) {
+  BQ_CHECK_ARG(valid_dtype(dtype), "unknown dtype %d", dtype);
+  BQ_CHECK_ARG(group_k >= 1, "group_k must be >= 1, got %lld", (long long)group_k);
+  return rmsnorm_impl(x, ldx, residual, ldr, weight, weight_offset, eps, M, K, group_k, dtype, q,
+                      ldq, s, nullptr, res_out, ldro, h_out, ldh, stream);
+}
+
+bq_status bq_mx_rmsnorm_quant(const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                              const void* weight, float weight_offset, float eps, int64_t M,
+                              int64_t K, void* q, int64_t ldq, void* sf, void* res_out,
+                              int64_t ldro, void* h_out, int64_t ldh, void* stream) {
+  bq_status st = mx_quant_check(x, M, K, ldx, q, ldq, sf);
+  if (st != BQ_OK) return st;
+  return rmsnorm_impl(x, ldx, residual, ldr, weight, weight_offset, eps, M, K, 32, bq::kMxFp8, q,
+                      ldq, nullptr, sf, res_out, ldro, h_out, ldh, stream);
+}
+
+bq_status bq_rope_frequencies(int64_t rot_dim, double base, int scaling, double factor,
+                              int64_t orig_max_pos, double beta_fast, double beta_slow,
+                              double* turns, float* mscale) {
+  BQ_CHECK_ARG(rot_dim >= 2 && rot_dim % 2 == 0, "rot_dim must be even and >= 2, got %lld",
+               (long long)rot_dim);
+  BQ_CHECK_ARG(scaling >= BQ_ROPE_PLAIN && scaling <= BQ_ROPE_YARN, "unknown scaling %d", scaling);
+  BQ_CHECK_ARG(std::isfinite(base) && base > 1.0, "base must be > 1");
+  BQ_CHECK_ARG(turns && mscale, "turns and mscale must not be NULL");
+  if (scaling != BQ_ROPE_PLAIN)
+    BQ_CHECK_ARG(std::isfinite(factor) && factor >= 1.0, "factor must be >= 1");
+  if (scaling == BQ_ROPE_NTK) BQ_CHECK_ARG(rot_dim >= 4, "BQ_ROPE_NTK needs rot_dim >= 4");
+  if (scaling == BQ_ROPE_YARN)
+    BQ_CHECK_ARG(orig_max_pos >= 1 && std::isfinite(beta_fast) && std::isfinite(beta_slow) &&
+                     beta_fast > beta_slow,
+                 "BQ_ROPE_YARN needs orig_max_pos >= 1 and beta_fast > beta_slow");
+  const double two_pi = 6.283185307179586476925286766559;
+  const double d = (double)rot_dim;
+  if (scaling == BQ_ROPE_NTK) base *= std::pow(factor, d / (d - 2.0));
+  for (int64_t i = 0; i < rot_dim / 2; ++i) {
+    double t = std::pow(base, -2.0 * (double)i / d) / two_pi;
+    if (scaling == BQ_ROPE_LINEAR) t /= factor;
+    if (scaling == BQ_ROPE_YARN) {
+      const double r = (double)orig_max_pos * t;
+      const double g = std::min(1.0, std::max(0.0, (r - beta_slow) / (beta_fast - beta_slow)));
+      t = (1.0 - g) * (t / factor) + g * t;
+    }
+    turns[i] = t;
+  }
+  *mscale = scaling == BQ_ROPE_YARN ? (float)(1.0 + 0.1 * std::log(factor)) : 1.0f;
+  return ok();
+}
+
+bq_status bq_rope(const void* x, int64_t ldt, int64_t ldh, const int32_t* positions,
+                  const double* turns, int64_t T, int64_t H, int64_t D, int64_t rot_dim,
+                  int layout, float mscale, void* out, int64_t ldot, int64_t ldoh,
+                  void* stream) {
+  BQ_CHECK_ARG(layout == BQ_ROPE_HALF || layout == BQ_ROPE_INTERLEAVED, "unknown layout %d",
+               layout);
+  BQ_CHECK_ARG(T >= 0 && H >= 0 && D >= 1, "need T >= 0, H >= 0, D >= 1");
+  BQ_CHECK_ARG(rot_dim >= 0 && rot_dim % 2 == 0 && rot_dim <= D,
+               "rot_dim must be even and in [0, D], got %lld", (long long)rot_dim);
+  BQ_CHECK_ARG(ldt >= 0 && ldh >= 0 && ldot >= 0 && ldoh >= 0, "strides must be >= 0");
+  BQ_CHECK_ARG(T <= 1 || H <= 1 || ldot >= (H - 1) * ldoh + D || ldoh >= (T - 1) * ldot + D,
+               "out: heads and tokens overlap");
+  BQ_CHECK_ARG((T <= 1 || ldot >= D) && (H <= 1 || ldoh >= D), "out: strides must be >= D");
+  if (T == 0 || H == 0) return ok();
+  BQ_CHECK_ARG(x && out && positions && (rot_dim == 0 || turns),
+               "x, positions, turns and out must not be NULL");
+  BQ_CHECK_ARG(out != x || (ldot == ldt && ldoh == ldh), "in place needs the same strides");
+  bq::RopeArgs a{};
+  a.x = static_cast<const uint16_t*>(x); a.ldt = ldt; a.ldh = ldh;
+  a.out = static_cast<uint16_t*>(out); a.ldot = ldot; a.ldoh = ldoh;
+  a.pos = positions; a.turns = turns;
+  a.T = T; a.H = H; a.D = D; a.rot = rot_dim;
+  a.interleaved = layout == BQ_ROPE_INTERLEAVED; a.mscale = mscale;
+  BQ_CHECK_CUDA(bq::launch_rope(a, as_stream(stream)), "rope launch");
+  return ok();
+}
+
+// What both cache calls check of the cache and of the batch.
+static bq_status kv_check(int64_t ld_table, int64_t table_cols, int64_t B, int64_t T, int64_t Hkv,
+                          int64_t D, int64_t n_pages, int64_t page_size, int64_t block_t,
+                          int dtype) {
+  BQ_CHECK_ARG(valid_dtype(dtype), "unknown dtype %d", dtype);
+  BQ_CHECK_ARG(B >= 0 && T >= 0 && n_pages >= 0, "B, T and n_pages must be >= 0");
+  BQ_CHECK_ARG(Hkv >= 1 && D >= 1, "Hkv and D must be >= 1");
+  BQ_CHECK_ARG(page_size >= 1 && block_t >= 1 && page_size % block_t == 0,
+               "block_t (%lld) must divide page_size (%lld)", (long long)block_t,
+               (long long)page_size);
+  BQ_CHECK_ARG(table_cols >= 0 && ld_table >= table_cols, "ld_table must be >= table_cols >= 0");
+  if (Hkv > 65535 || page_size > 65536 || D > 16384 || T > INT32_MAX - 1 || B > (1 << 28) ||
+      n_pages > INT32_MAX || table_cols > INT32_MAX / page_size)
+    return fail(BQ_ERR_UNSUPPORTED,
+                "the cache calls take Hkv <= 65535, page_size <= 65536, D <= 16384, B <= 2^28 and "
+                "rows, pages and sequence lengths within int32");
+  return BQ_OK;
+}
+
+bq_status bq_kv_append(const void* k, int64_t ldk, int64_t hk, const void* v, int64_t ldv,
+                       int64_t hv, const int32_t* seq_offsets, const int32_t* kv_lens,
+                       const int32_t* page_table, int64_t ld_table, int64_t table_cols, int64_t B,
+                       int64_t T, int64_t Hkv, int64_t D, int64_t n_pages, int64_t page_size,
+                       int64_t block_t, int dtype, void* k_codes, void* v_codes, float* k_scales,
+                       float* v_scales, void* stream) {
+  bq_status st = kv_check(ld_table, table_cols, B, T, Hkv, D, n_pages, page_size, block_t, dtype);
+  if (st != BQ_OK) return st;
+  BQ_CHECK_ARG(ldk >= 0 && hk >= 0 && ldv >= 0 && hv >= 0, "strides must be >= 0");
+  if (T == 0 || B == 0) return ok();
+  BQ_CHECK_ARG(k && v && seq_offsets && kv_lens && page_table && k_codes && v_codes && k_scales &&
+                   v_scales,
+               "the token, batch and cache arrays must not be NULL");
+  unsigned* w = nullptr;
+  st = status_word(&w);
+  if (st != BQ_OK) return st;
+  bq::AppendArgs a{};
+  a.c = {static_cast<uint8_t*>(k_codes), static_cast<uint8_t*>(v_codes), k_scales, v_scales,
+         n_pages, (int)Hkv, (int)page_size, (int)D, (int)block_t, dtype};
+  a.b = {seq_offsets, kv_lens, page_table, ld_table, (int)table_cols, (int)B, T};
+  a.k = static_cast<const uint16_t*>(k); a.ldk = ldk; a.hk = hk;
+  a.v = static_cast<const uint16_t*>(v); a.ldv = ldv; a.hv = hv;
+  a.status = w;
+  BQ_CHECK_CUDA(bq::launch_kv_append(a, as_stream(stream)), "kv_append launch");
+  return ok();
+}
+
+static bq_status attn_check(int64_t Hq, int64_t Hkv, int64_t D, int64_t max_q_len,
+                            int64_t max_kv_len) {
+  BQ_CHECK_ARG(Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0,
+               "Hq (%lld) must be a multiple of Hkv (%lld)", (long long)Hq, (long long)Hkv);
+  BQ_CHECK_ARG(max_q_len >= 0 && max_kv_len >= 0, "max_q_len and max_kv_len must be >= 0");
+  if (D < 1 || D > 256 || Hq > 65535 || max_q_len > INT32_MAX || max_kv_len > INT32_MAX)
+    return fail(BQ_ERR_UNSUPPORTED,
+                "attention takes D in [1, 256], Hq <= 65535 and lengths within int32");
+  return BQ_OK;
+}
+
+// bq_kv_attention workspace: [64 KiB left untouched, as in bq_mx_linear] [partials].
+bq_status bq_kv_attention_workspace_size(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                                         int64_t max_q_len, int64_t max_kv_len, int64_t page_size,
+                                         int64_t block_t, size_t* bytes) {
+  BQ_CHECK_ARG(bytes, "bytes must not be NULL");
+  bq_status st = kv_check(0, 0, B, T, Hkv, D, 0, page_size, block_t, BQ_INT8);
+  if (st == BQ_OK) st = attn_check(Hq, Hkv, D, max_q_len, max_kv_len);
+  if (st != BQ_OK) return st;
+  const size_t n = bq::attn_workspace_bytes(B, T, Hq, Hkv, D, max_q_len, max_kv_len, page_size,
+                                            block_t);
+  *bytes = n ? n + bq::kDecodeCounterBytes : 0;
+  return ok();
+}
+
+bq_status bq_kv_attention(const void* q, int64_t ldq, int64_t hq, const int32_t* seq_offsets,
+                          const int32_t* kv_lens, const int32_t* page_table, int64_t ld_table,
+                          int64_t table_cols, int64_t B, int64_t T, int64_t Hq, int64_t Hkv,
+                          int64_t D, int64_t max_q_len, int64_t max_kv_len, const void* k_codes,
+                          const void* v_codes, const float* k_scales, const float* v_scales,
+                          int64_t n_pages, int64_t page_size, int64_t block_t, int dtype,
+                          float scale, int causal, int64_t window, void* out, int64_t ldo,
+                          int64_t ho, float* lse, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+  bq_status st = kv_check(ld_table, table_cols, B, T, Hkv, D, n_pages, page_size, block_t, dtype);
+  if (st == BQ_OK) st = attn_check(Hq, Hkv, D, max_q_len, max_kv_len);
+  if (st != BQ_OK) return st;
+  BQ_CHECK_ARG(std::isfinite(scale), "scale must be finite");
+  BQ_CHECK_ARG(window >= 0 && (window == 0 || causal), "a window needs causal attention");
+  BQ_CHECK_ARG(ldq >= 0 && hq >= 0, "strides must be >= 0");
+  BQ_CHECK_ARG((T <= 1 || ldo >= D) && (Hq <= 1 || ho >= D) &&
+                   (T <= 1 || Hq <= 1 || ldo >= (Hq - 1) * ho + D || ho >= (T - 1) * ldo + D),
+               "out: rows or heads overlap");
+  if (T == 0 || B == 0) return ok();
+  BQ_CHECK_ARG(q && seq_offsets && kv_lens && out, "q, seq_offsets, kv_lens and out must not be "
+                                                   "NULL");
+  BQ_CHECK_ARG(table_cols == 0 || n_pages == 0 ||
+                   (page_table && k_codes && v_codes && k_scales && v_scales),
+               "page_table and the cache arrays must not be NULL");
+  const size_t parts = bq::attn_workspace_bytes(B, T, Hq, Hkv, D, max_q_len, max_kv_len,
+                                                page_size, block_t);
+  const size_t need = parts ? parts + bq::kDecodeCounterBytes : 0;
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need))
+    return fail(BQ_ERR_WORKSPACE, "bq_kv_attention needs %zu workspace bytes, got %zu", need,
+                workspace ? workspace_bytes : (size_t)0);
+  if (need > 0 && !aligned16(workspace))
+    return fail(BQ_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
+  unsigned* w = nullptr;
+  st = status_word(&w);
+  if (st != BQ_OK) return st;
+  bq::AttnArgs a{};
+  a.c = {static_cast<uint8_t*>(const_cast<void*>(k_codes)),
+         static_cast<uint8_t*>(const_cast<void*>(v_codes)), const_cast<float*>(k_scales),
+         const_cast<float*>(v_scales), n_pages, (int)Hkv, (int)page_size, (int)D, (int)block_t,
+         dtype};
+  a.b = {seq_offsets, kv_lens, page_table, ld_table, (int)table_cols, (int)B, T};
+  a.q = static_cast<const uint16_t*>(q); a.ldq = ldq; a.hq = hq;
+  a.out = static_cast<uint16_t*>(out); a.ldo = ldo; a.ho = ho;
+  a.lse = lse; a.Hq = (int)Hq; a.max_q = (int)max_q_len; a.max_kv = (int)max_kv_len;
+  a.scale = scale; a.causal = causal != 0;
+  a.window = (int)std::min<int64_t>(window, INT32_MAX);
+  a.status = w;
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+  BQ_CHECK_CUDA(bq::launch_kv_attention(a, need ? base + bq::kDecodeCounterBytes : nullptr,
+                                        as_stream(stream)),
+                "kv_attention launch");
   return ok();
 }
 

@@ -55,6 +55,8 @@
  *  - Weight scales are [Nb][Kb] row-major as on the block-wise INT8 page.
  *  - The MXFP8 calls (bq_mx_*) keep their E8M0 scales in the tensor-core
  *    atom layout described before bq_mx_scale_bytes.
+ *  - The operators between two linears (norm, rotary positions, cache,
+ *    attention) stand at the end, with the cache's layout.
  */
 #ifndef BQ_H_
 #define BQ_H_
@@ -474,6 +476,145 @@ bq_status bq_moe_silu_mul_quant(const void* y, int64_t ldy, int64_t R, int64_t I
 bq_status bq_moe_combine(const void* y, int64_t ldy, const int32_t* inv_perm,
                          const float* topk_w, int64_t T, int64_t topk, int64_t H, void* out,
                          int64_t ldo, void* stream);
+
+/* ---- between two linears: norm, rotary positions, cache, attention ----
+ * The operators that stand between two block-scaled linears of a decoder
+ * layer.  None of them is on the pages; their quantisation follows the rules
+ * above (s = amax / Q, IEEE division, round to nearest even), so that their
+ * codes and scales are what bq_gemm and bq_mx_gemm take. */
+
+/* RMS norm with the residual's addition and an 8-bit output:
+ *   r[m, k] = bf16(x[m, k] + residual[m, k])     (r = x if residual is NULL)
+ *   y[m, k] = r[m, k] / sqrt(mean_k r[m, k]^2 + eps) * (weight[k] + weight_offset)
+ *   q, s    = the 1 x group_k quantisation of y, as bq_quant_act
+ * y is fp32 and is quantised unrounded (a separate norm and bq_quant_act
+ * would round it to bf16 in between).  x: bf16 [M, K] (row stride ldx >= K);
+ * residual: bf16 [M, K] (row stride ldr) or NULL; weight: bf16 [K];
+ * weight_offset: 0, or 1 for weights stored as their difference from 1.
+ * q: codes [M, K] (row stride ldq), s: fp32 [ceil(K/group_k)][M].
+ * res_out: r as bf16 [M, K] (row stride ldro), or NULL; it may be residual or
+ * x itself (same pointer and stride).  h_out: y rounded to bf16 [M, K] (row
+ * stride ldh), or NULL.  Other overlaps of inputs and outputs are not allowed.
+ * K <= 98304 (else BQ_ERR_UNSUPPORTED).  No workspace. */
+bq_status bq_rmsnorm_quant(const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                           const void* weight, float weight_offset, float eps, int64_t M,
+                           int64_t K, int64_t group_k, int dtype, void* q, int64_t ldq, float* s,
+                           void* res_out, int64_t ldro, void* h_out, int64_t ldh, void* stream);
+
+/* The same norm with the MXFP8 quantisation of y (rule and scale layout of
+ * bq_mx_quant_act): q e4m3 [M, K] (row stride ldq, 4-byte aligned rows), sf
+ * the scale array (bq_mx_scale_bytes(M, K) bytes).  K a multiple of 128. */
+bq_status bq_mx_rmsnorm_quant(const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                              const void* weight, float weight_offset, float eps, int64_t M,
+                              int64_t K, void* q, int64_t ldq, void* sf, void* res_out,
+                              int64_t ldro, void* h_out, int64_t ldh, void* stream);
+
+typedef enum bq_rope_layout {
+    BQ_ROPE_HALF = 0,         /* pair i = dimensions i and i + rot_dim / 2 */
+    BQ_ROPE_INTERLEAVED = 1   /* pair i = dimensions 2i and 2i + 1 */
+} bq_rope_layout;
+
+/* Frequencies scaled for contexts longer than the trained one. */
+typedef enum bq_rope_scaling {
+    BQ_ROPE_PLAIN = 0,    /* theta_i = base^(-2i / rot_dim) */
+    BQ_ROPE_LINEAR = 1,   /* theta_i / factor (position interpolation) */
+    BQ_ROPE_NTK = 2,      /* base * factor^(rot_dim / (rot_dim - 2)) in place of base */
+    BQ_ROPE_YARN = 3      /* by wavelength, see below */
+} bq_rope_scaling;
+
+/* Frequencies of bq_rope (host only; no GPU is needed).  Writes turns[i] =
+ * theta_i / (2 pi) for i < rot_dim / 2 into a HOST array of doubles, which the
+ * caller copies to the device, and the factor for bq_rope's mscale into
+ * *mscale.  BQ_ROPE_YARN (Peng et al., "YaRN", 2023, sections 3.2-3.4): with
+ * rotations r_i = orig_max_pos * turns[i] and g = clamp((r_i - beta_slow) /
+ * (beta_fast - beta_slow), 0, 1), theta_i becomes (1 - g) theta_i / factor +
+ * g theta_i, and mscale = 1 + 0.1 ln(factor); mscale is 1 for the others.
+ * rot_dim even and >= 2 (>= 4 for BQ_ROPE_NTK), base > 1, factor >= 1,
+ * and for BQ_ROPE_YARN orig_max_pos >= 1 and beta_fast > beta_slow. */
+bq_status bq_rope_frequencies(int64_t rot_dim, double base, int scaling, double factor,
+                              int64_t orig_max_pos, double beta_fast, double beta_slow,
+                              double* turns, float* mscale);
+
+/* Rotary positions on H heads of T tokens: with c, s the cosine and sine of
+ * 2 pi * positions[t] * turns[i], times mscale, the pair (a, b) of dimensions
+ * (see bq_rope_layout) becomes (a c - b s, b c + a s); dimensions past rot_dim
+ * are copied.  fp32, each result rounded once to bf16; the angle is reduced in
+ * fp64, so far positions are as exact as near ones.
+ * x: bf16, element (t, h, d) at x[t * ldt + h * ldh + d]; out likewise with
+ * ldot, ldoh; out may be x itself (same pointer and strides), other overlaps
+ * are not allowed.  positions: int32 [T], any sign (-p undoes p);
+ * turns: DEVICE fp64 [rot_dim / 2].  0 <= rot_dim <= D, even. */
+bq_status bq_rope(const void* x, int64_t ldt, int64_t ldh, const int32_t* positions,
+                  const double* turns, int64_t T, int64_t H, int64_t D, int64_t rot_dim,
+                  int layout, float mscale, void* out, int64_t ldot, int64_t ldoh,
+                  void* stream);
+
+/* The paged 8-bit cache of keys and values (bq_kv_append writes it,
+ * bq_kv_attention reads it).
+ *   codes  k_codes, v_codes: one byte each, [n_pages][Hkv][page_size][D], dense;
+ *   scales k_scales, v_scales: fp32 [n_pages][Hkv][page_size / block_t], one
+ *          for each block of block_t consecutive tokens of a page and head
+ *          (block_t divides page_size); value = code * scale.
+ * A call works on B sequences.  seq_offsets: int32 [B + 1], nondecreasing from
+ * 0; rows [seq_offsets[b], seq_offsets[b+1]) of the call's token arrays (T
+ * rows) are the LAST tokens of sequence b.  kv_lens: int32 [B], the length of
+ * each sequence with those tokens.  page_table: int32 [B][table_cols] (row
+ * stride ld_table): token t of sequence b is slot t % page_size of page
+ * page_table[b][t / page_size].  All three are DEVICE arrays and are read by
+ * the kernels alone; entries that cannot be used (offsets that decrease or
+ * pass T, a length past table_cols * page_size, a page outside [0, n_pages))
+ * are skipped and recorded in the device status word as BQ_ERR_INVALID_ARG.
+ * Rows at and behind seq_offsets[B] are neither read nor written. */
+
+/* Append: quantise the new tokens' keys and values (bf16, element (t, h, d) at
+ * k[t * ldk + h * hk + d], v likewise) into the cache.  For each touched block
+ * (block_t tokens, head; keys and values apart), with n_old tokens of the
+ * sequence already in it:
+ *   s' = max(s_old, amax(new) / Q), s_old = 0 if n_old == 0;
+ *   new codes as bq_quant_act with scale s';
+ *   if s' > s_old, the n_old old codes become the codes of (q_old * s_old).
+ * Slots behind the last token keep their bytes.  A sequence must hold its new
+ * tokens (kv_lens[b] >= their number).  A page that a call writes belongs to
+ * one sequence of that call.  Writing the same tokens again changes nothing. */
+bq_status bq_kv_append(const void* k, int64_t ldk, int64_t hk, const void* v, int64_t ldv,
+                       int64_t hv, const int32_t* seq_offsets, const int32_t* kv_lens,
+                       const int32_t* page_table, int64_t ld_table, int64_t table_cols, int64_t B,
+                       int64_t T, int64_t Hkv, int64_t D, int64_t n_pages, int64_t page_size,
+                       int64_t block_t, int dtype, void* k_codes, void* v_codes, float* k_scales,
+                       float* v_scales, void* stream);
+
+/* Bytes of workspace bq_kv_attention needs (0 is possible). */
+bq_status bq_kv_attention_workspace_size(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                                         int64_t max_q_len, int64_t max_kv_len, int64_t page_size,
+                                         int64_t block_t, size_t* bytes);
+
+/* Attention of T query rows, Hq heads each, over the cache.  Query head h
+ * reads key head h / (Hq / Hkv).  Row i of the n rows of sequence b stands at
+ * position p = kv_lens[b] - n + i and sees the keys j < kv_lens[b] with, if
+ * causal != 0, j <= p and, if window > 0 (causal only), j > p - window:
+ *   z_j = scale * (q . k_j),  out = sum_j softmax(z)_j v_j,  lse = ln sum_j exp(z_j)
+ * k_j, v_j = code * scale.  Sums and softmax statistics are fp32; out is
+ * rounded once to bf16.  A row that sees no key gives zeros and lse = -inf.
+ * Slots of a page behind kv_lens[b] may hold any bytes.  The keys and values
+ * that some row of the call sees, and the queries, must be finite.
+ * q: bf16, element (t, h, d) at q[t * ldq + h * hq + d]; out likewise with ldo,
+ * ho (no overlap with q); lse: fp32 [T][Hq] or NULL.  max_q_len and max_kv_len
+ * bound every sequence's rows and length (a longer sequence is skipped and
+ * recorded); they choose the kernel and the workspace, so a captured call
+ * stays valid while lengths grow up to them.  D <= 256.
+ * workspace: at least bq_kv_attention_workspace_size bytes, 16-byte aligned, no
+ * initialisation, nothing kept in it; calls sharing one must not overlap on
+ * the GPU.  Its first 64 KiB are left untouched, so the buffer of bq_gemm can
+ * serve here too. */
+bq_status bq_kv_attention(const void* q, int64_t ldq, int64_t hq, const int32_t* seq_offsets,
+                          const int32_t* kv_lens, const int32_t* page_table, int64_t ld_table,
+                          int64_t table_cols, int64_t B, int64_t T, int64_t Hq, int64_t Hkv,
+                          int64_t D, int64_t max_q_len, int64_t max_kv_len, const void* k_codes,
+                          const void* v_codes, const float* k_scales, const float* v_scales,
+                          int64_t n_pages, int64_t page_size, int64_t block_t, int dtype,
+                          float scale, int causal, int64_t window, void* out, int64_t ldo,
+                          int64_t ho, float* lse, void* workspace, size_t workspace_bytes,
+                          void* stream);
 
 #ifdef __cplusplus
 }
