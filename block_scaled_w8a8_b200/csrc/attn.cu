@@ -1,5 +1,5 @@
-// attn.cu -- attention over the paged 8-bit cache: the dispatch, and the
-// CUDA-core kernel that takes any head size and stride.
+// attn.cu -- attention over the paged 8-bit cache: the dispatch, the join of
+// split keys, and the CUDA-core kernel that takes any head size and stride.
 //
 // For row i of sequence b at position p_i = len_b - n_b + i, query head h and
 // its key head h / (Hq / Hkv):
@@ -10,13 +10,16 @@
 // Keys that no row may see are never read into a sum, whatever bytes they hold.
 #include <algorithm>
 
+#include "attn.h"
+#include "attn_common.cuh"
 #include "bq_common.cuh"
 #include "kv_common.cuh"
-#include "layer_ops.h"
 
 namespace bq {
 
 namespace {
+
+using attn::row_range;
 
 constexpr int kAnyWarps = 4;
 constexpr int kMaxD = 256;
@@ -45,9 +48,8 @@ __global__ void __launch_bounds__(kAnyWarps * 32) attn_any_kernel(const AttnArgs
     return;
   }
   if (t < s.row0 || t >= s.row0 + s.n) return;      // a row behind the last sequence
-  const int pos = s.len - s.n + (int)(t - s.row0);
-  const int hi = a.causal ? min(pos + 1, s.len) : s.len;
-  const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+  int lo, hi;
+  row_range(a, s, (int)(t - s.row0), lo, hi);
   const int hk = h / (a.Hq / a.c.H), D = a.c.D;
   const uint16_t* q = a.q + t * a.ldq + h * a.hq;
   float qv[kPer], o[kPer];
@@ -94,28 +96,103 @@ __global__ void __launch_bounds__(kAnyWarps * 32) attn_any_kernel(const AttnArgs
   if (a.lse && lane == 0) a.lse[t * a.Hq + h] = l == 0.f ? -INFINITY : m + logf(l);
 }
 
-}  // namespace
+// Joins the splits of a row in split order: a warp per (row, query head).
+constexpr int kMergeWarps = 4;
 
-size_t attn_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int64_t,
-                            int64_t, int64_t) {
-  return 0;
+__global__ void __launch_bounds__(kMergeWarps * 32)
+attn_merge_kernel(const AttnArgs a, const AttnParts p) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31;
+  const int64_t item = (int64_t)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+  const int64_t t = item / a.Hq;
+  const int h = (int)(item - t * a.Hq);
+  if (t >= a.b.T) return;
+  const int b = kv::last_at_most(a.b.B, t, [&](int i) { return (int64_t)a.b.off[i]; });
+  kv::Seq s;
+  if (!kv::load_seq(a.b, a.c.page, b, s) || s.n > a.max_q || s.len > a.max_kv || t < s.row0 ||
+      t >= s.row0 + s.n)
+    return;                          // recorded by the kernel before, or nobody's row
+  const float4* stat = reinterpret_cast<const float4*>(p.stat) + item * p.splits;
+  float m = -INFINITY, mo = -INFINITY, l = 0.f;
+  for (int i = lane; i < p.splits; i += 32) {
+    const float4 x = stat[i];
+    m = fmaxf(m, x.x);
+    mo = fmaxf(mo, x.z);
+  }
+  m = warp_max(m);
+  mo = warp_max(mo);
+  float acc[kMaxD / 32] = {};
+  for (int i = 0; i < p.splits; ++i) {
+    const float4 x = stat[i];
+    if (x.y == 0.f) continue;
+    l += x.y * attn::ex2(x.x - attn::finite(m));
+    const float f = attn::ex2(x.z - attn::finite(mo));
+    const float* o = p.o + (item * p.splits + i) * a.c.D;
+#pragma unroll
+    for (int e = 0; e < kMaxD / 32; ++e)
+      if (lane + 32 * e < a.c.D) acc[e] = fmaf(o[lane + 32 * e], f, acc[e]);
+  }
+#pragma unroll
+  for (int e = 0; e < kMaxD / 32; ++e)
+    if (lane + 32 * e < a.c.D) attn::write_row(a, t, h, lane + 32 * e, m, l, mo, acc[e]);
 }
 
-cudaError_t launch_kv_attention(const AttnArgs& a, void* ws, cudaStream_t st) {
-  (void)ws;
-  const int64_t items = a.b.T * a.Hq;
-  if (items == 0) return cudaSuccess;
+template <class... Args>
+cudaError_t launch_pdl(void (*kernel)(Args...), int64_t grid, int threads, cudaStream_t st,
+                       Args... args) {
+  if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((items + kAnyWarps - 1) / kAnyWarps));
-  cfg.blockDim = dim3(kAnyWarps * 32);
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.stream = st;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  if (a.c.dtype == kInt8) return cudaLaunchKernelEx(&cfg, attn_any_kernel<kInt8>, a);
-  return cudaLaunchKernelEx(&cfg, attn_any_kernel<kFp8>, a);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// How the keys of a call are split, from the call's sizes alone.
+int plan_splits(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_q, int64_t max_kv,
+                int64_t page) {
+  if (!attn_decode_takes(D, page)) return 1;
+  return attn_decode_splits(B, Hkv, max_q * (Hq / Hkv), max_kv);
+}
+
+}  // namespace
+
+size_t attn_workspace_bytes(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                            int64_t max_q, int64_t max_kv, int64_t page, int64_t bt) {
+  (void)bt;
+  return attn_part_bytes(T * Hq, plan_splits(B, Hq, Hkv, D, max_q, max_kv, page), D);
+}
+
+cudaError_t launch_attn_merge(const AttnArgs& a, const AttnParts& p, cudaStream_t st) {
+  const int64_t items = a.b.T * a.Hq;
+  return launch_pdl(attn_merge_kernel, (items + kMergeWarps - 1) / kMergeWarps, kMergeWarps * 32,
+                    st, a, p);
+}
+
+cudaError_t launch_kv_attention(const AttnArgs& a, void* ws, cudaStream_t st) {
+  const int64_t items = a.b.T * a.Hq;
+  const bool aligned = ((reinterpret_cast<uintptr_t>(a.c.k) | reinterpret_cast<uintptr_t>(a.c.v)) &
+                        15) == 0;
+  if (aligned && a.max_q > 0 && attn_decode_takes(a.c.D, a.c.page)) {
+    AttnParts p{};
+    p.splits = plan_splits(a.b.B, a.Hq, a.c.H, a.c.D, a.max_q, a.max_kv, a.c.page);
+    if (p.splits > 1) {
+      p.stat = static_cast<float*>(ws);
+      p.o = p.stat + 4 * items * p.splits;
+    }
+    cudaError_t e = launch_attn_decode(a, p, st);
+    if (e == cudaSuccess && p.splits > 1) e = launch_attn_merge(a, p, st);
+    return e;
+  }
+  const int64_t grid = (items + kAnyWarps - 1) / kAnyWarps;
+  return a.c.dtype == kInt8 ? launch_pdl(attn_any_kernel<kInt8>, grid, kAnyWarps * 32, st, a)
+                            : launch_pdl(attn_any_kernel<kFp8>, grid, kAnyWarps * 32, st, a);
 }
 
 }  // namespace bq

@@ -1,0 +1,30 @@
+// attn.h -- what the attention kernels share on the host side: the split of
+// the keys over CTAs and its workspace, and the kernels' launchers.
+#pragma once
+
+#include "layer_ops.h"
+
+namespace bq {
+
+// Partial results of a row (token t, query head h), one per split: fp32 O[D] of
+// the weights 2^(z + lg2 vs - mo), and {m, l, mo}: the running maximum of the
+// scores z (in log2 units), l = sum 2^(z - m), and O's own reference mo.  A
+// split that saw no key of the row has l = 0 and writes no O.
+struct AttnParts {
+  float* o;        // [T * Hq][splits][D]
+  float* stat;     // [T * Hq][splits][4]
+  int splits;      // 1: no partials, the kernel writes the result itself
+};
+
+inline size_t attn_part_bytes(int64_t rows, int splits, int64_t D) {
+  return splits <= 1 ? 0 : (size_t)rows * (size_t)splits * (size_t)(D + 4) * sizeof(float);
+}
+
+cudaError_t launch_attn_merge(const AttnArgs& a, const AttnParts& p, cudaStream_t st);
+
+// Few rows per sequence and key head (decoding): attn_decode.cu.
+bool attn_decode_takes(int64_t D, int64_t page);
+int attn_decode_splits(int64_t B, int64_t Hkv, int64_t rows, int64_t max_kv);
+cudaError_t launch_attn_decode(const AttnArgs& a, const AttnParts& p, cudaStream_t st);
+
+}  // namespace bq

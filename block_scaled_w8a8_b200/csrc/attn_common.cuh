@@ -1,0 +1,134 @@
+// attn_common.cuh -- device helpers shared by the attention kernels: which keys
+// a row sees, how the keys are split, codes to fp16, and a row's result.
+#pragma once
+
+#include "bq_common.cuh"
+#include "kv_common.cuh"
+#include "layer_ops.h"
+
+namespace bq {
+namespace attn {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct Range { int lo, hi; };
+
+// Keys [lo, hi) that row i of sequence s sees (hi <= lo: none).
+__device__ __forceinline__ void row_range(const AttnArgs& a, const kv::Seq& s, int i, int& lo,
+                                          int& hi) {
+  const int pos = s.len - s.n + i;
+  hi = a.causal ? min(pos + 1, s.len) : s.len;
+  lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+}
+
+// Keys that some row of i_lo .. i_hi sees: both ends grow with the row.
+__device__ __forceinline__ Range tile_range(const AttnArgs& a, const kv::Seq& s, int i_lo,
+                                            int i_hi) {
+  Range r;
+  int unused;
+  row_range(a, s, i_lo, r.lo, unused);
+  row_range(a, s, i_hi, unused, r.hi);
+  if (r.hi < r.lo) r.hi = r.lo;
+  return r;
+}
+
+// Part `split` of `splits` of the keys, cut at multiples of `step` from token
+// 0 on (so that no group of `step` tokens is shared); may be empty.
+__device__ __forceinline__ Range split_range(const Range& all, int split, int splits, int step) {
+  const int g0 = all.lo / step, g1 = (all.hi + step - 1) / step;
+  const int per = (max(g1 - g0, 0) + splits - 1) / splits;
+  Range r;
+  r.lo = (int)min((int64_t)g1, g0 + (int64_t)split * per) * step;
+  r.hi = (int)min((int64_t)all.hi, min((int64_t)g1, g0 + ((int64_t)split + 1) * per) * step);
+  return r;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A running maximum as the reference of a difference: 0 while nothing was seen.
+__device__ __forceinline__ float finite(float m) { return m == -INFINITY ? 0.f : m; }
+
+__device__ __forceinline__ uint4 ld_codes16(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
+__device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Four codes (byte i = code i) as two fp16 pairs, exactly.
+template <int DT>
+__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if constexpr (DT == kInt8) {
+    // q + 128 as the low byte of the fp16 number 1024 + (q + 128), less 1152
+    const uint32_t u = w ^ 0x80808080u;
+    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140);
+    const uint32_t b = __byte_perm(u, 0x64646464u, 0x4342);
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(0x64806480u));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0x64806480u));
+  } else {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi) : "r"(w));
+  }
+}
+
+// Powers of two that bring a row of largest magnitude amax to 2^14 .. 2^15 and
+// back; 1 for a row of zeros or one that is not finite.
+__device__ __forceinline__ void row_power(float amax, float& up, float& down) {
+  const int ef = (int)(__float_as_uint(amax) >> 23);
+  int k = (ef == 0 || ef >= 255) ? 0 : min(14 - (ef - 127), 126);
+  up = __uint_as_float((uint32_t)(127 + k) << 23);
+  down = __uint_as_float((uint32_t)(127 - k) << 23);
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4],
+                                        const uint32_t (&b)[2]) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+
+// The 8 x 8 matrix of 16-bit elements that a warp holds (lane 4 i + j: row i,
+// columns 2j, 2j + 1), transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// out[tok, head, d] and, from the thread of d = 0, lse: from the maximum m and
+// sum l of the scores (log2 units) and acc = O in units of 2^mo.
+__device__ __forceinline__ void write_row(const AttnArgs& a, int64_t tok, int head, int d, float m,
+                                          float l, float mo, float acc) {
+  // l == 0: the row saw no key; mo == -inf: only values with a scale of 0
+  const bool none = l == 0.f || mo == -INFINITY;
+  const float v = none ? 0.f : acc * __fdiv_rn(ex2(mo - finite(m)), l);
+  a.out[tok * a.ldo + (int64_t)head * a.ho + d] = float_to_bf16_bits(v);
+  if (a.lse && d == 0)
+    a.lse[tok * a.Hq + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+}  // namespace attn
+}  // namespace bq
