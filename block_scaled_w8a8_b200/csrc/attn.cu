@@ -154,11 +154,22 @@ cudaError_t launch_pdl(void (*kernel)(Args...), int64_t grid, int threads, cudaS
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// How the keys of a call are split, from the call's sizes alone.
-int plan_splits(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_q, int64_t max_kv,
-                int64_t page) {
-  if (!attn_decode_takes(D, page)) return 1;
-  return attn_decode_splits(B, Hkv, max_q * (Hq / Hkv), max_kv);
+// The kernel of a call and how it splits the keys, from the call's sizes alone.
+enum class Path { kAny, kDecode, kTc };
+
+// Up to 32 rows per key head the decode kernel streams the codes at most twice;
+// beyond that the tensor cores win.
+constexpr int64_t kDecodeRows = 32;
+
+Path plan_path(int64_t D, int64_t page, int64_t rows) {
+  if (rows > kDecodeRows && attn_tc_takes(D, page)) return Path::kTc;
+  return attn_decode_takes(D, page) ? Path::kDecode : Path::kAny;
+}
+
+int plan_splits(Path path, int64_t B, int64_t Hq, int64_t Hkv, int64_t max_q, int64_t max_kv) {
+  if (path == Path::kTc) return attn_tc_splits(B, Hkv, max_q, Hq / Hkv, max_kv);
+  if (path == Path::kDecode) return attn_decode_splits(B, Hkv, max_q * (Hq / Hkv), max_kv);
+  return 1;
 }
 
 }  // namespace
@@ -166,7 +177,8 @@ int plan_splits(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_q, in
 size_t attn_workspace_bytes(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
                             int64_t max_q, int64_t max_kv, int64_t page, int64_t bt) {
   (void)bt;
-  return attn_part_bytes(T * Hq, plan_splits(B, Hq, Hkv, D, max_q, max_kv, page), D);
+  const Path path = plan_path(D, page, max_q * (Hq / Hkv));
+  return attn_part_bytes(T * Hq, plan_splits(path, B, Hq, Hkv, max_q, max_kv), D);
 }
 
 cudaError_t launch_attn_merge(const AttnArgs& a, const AttnParts& p, cudaStream_t st) {
@@ -179,14 +191,16 @@ cudaError_t launch_kv_attention(const AttnArgs& a, void* ws, cudaStream_t st) {
   const int64_t items = a.b.T * a.Hq;
   const bool aligned = ((reinterpret_cast<uintptr_t>(a.c.k) | reinterpret_cast<uintptr_t>(a.c.v)) &
                         15) == 0;
-  if (aligned && a.max_q > 0 && attn_decode_takes(a.c.D, a.c.page)) {
+  const Path path = plan_path(a.c.D, a.c.page, (int64_t)a.max_q * (a.Hq / a.c.H));
+  if (aligned && a.max_q > 0 && path != Path::kAny) {
     AttnParts p{};
-    p.splits = plan_splits(a.b.B, a.Hq, a.c.H, a.c.D, a.max_q, a.max_kv, a.c.page);
+    p.splits = plan_splits(path, a.b.B, a.Hq, a.c.H, a.max_q, a.max_kv);
     if (p.splits > 1) {
       p.stat = static_cast<float*>(ws);
       p.o = p.stat + 4 * items * p.splits;
     }
-    cudaError_t e = launch_attn_decode(a, p, st);
+    cudaError_t e =
+        path == Path::kTc ? launch_attn_tc(a, p, st) : launch_attn_decode(a, p, st);
     if (e == cudaSuccess && p.splits > 1) e = launch_attn_merge(a, p, st);
     return e;
   }

@@ -27,4 +27,10 @@ bool attn_decode_takes(int64_t D, int64_t page);
 int attn_decode_splits(int64_t B, int64_t Hkv, int64_t rows, int64_t max_kv);
 cudaError_t launch_attn_decode(const AttnArgs& a, const AttnParts& p, cudaStream_t st);
 
+// Many rows (prompts): attn_tc.cu.
+bool attn_tc_takes(int64_t D, int64_t page);
+int64_t attn_tc_tiles(int64_t max_q, int64_t group);
+int attn_tc_splits(int64_t B, int64_t Hkv, int64_t max_q, int64_t group, int64_t max_kv);
+cudaError_t launch_attn_tc(const AttnArgs& a, const AttnParts& p, cudaStream_t st);
+
 }  // namespace bq
