@@ -6,9 +6,10 @@
 //   warps 0-3, 4-7  softmax of row tile 0, 1: a thread per row reads its 128
 //                   scores from tensor memory, writes the weights back as fp16
 //                   over them, and at the end divides the output row;
-//   warps 8-11      converters: codes from memory (requested a tile ahead) to
-//                   fp16 tiles in shared memory, K and V each twice buffered,
-//                   and the tile's scales;
+//   warps 8-11      keys: codes from memory (requested a tile ahead) to fp16
+//                   tiles in shared memory, twice buffered, and the scales of
+//                   the tile's keys and values;
+//   warps 13-15     values: the same;
 //   warp 12         issues the products: S_a = Q_a K^T (both operands in shared
 //                   memory) and O_a += P_a V (P_a from tensor memory, V as it
 //                   lies, its rows running along the reduction).
@@ -17,13 +18,13 @@
 // Tensor memory: S_0, S_1 (128 columns each, P_a in the first 64 of S_a), O_0, O_1.
 //
 // Weights: with y = z + lg2 vs (z the score in log2 units, vs the value's block
-// scale) and mo a bound on the row's y so far, the weight is 2^(y - mo), so the
-// product with the bare codes is the value sum in units of 2^mo whatever the
-// scales are, and l += weight / vs is the softmax sum in the same units: one
-// exponential serves both.  Value scales below 2^-100 count as 2^-100 there.
-// mo is raised (and O rescaled) only when y passes it by more than 8: weights
-// stay below 2^8, far from fp16's end, and a rescale is rare.  The fp16
-// rounding of a weight is half a step of 2^-11; scores, sums and O are fp32.
+// scale) and mo a reference of the row, the weight is 2^(y - mo), so the product
+// with the bare codes is the value sum in units of 2^mo whatever the scales are,
+// and l += weight / vs is the softmax sum in the same units: one exponential
+// serves both.  Value scales below 2^-100 count as 2^-100 there.  mo is raised
+// (and O rescaled) only when y passes it by more than 8: weights stay below 2^8,
+// far from fp16's end, and a rescale is rare.  The fp16 rounding of a weight is
+// half a step of 2^-11; scores, sums and O are fp32.
 // Queries are scaled per row by a power of two and exact in fp16, as in
 // attn_decode.cu.  Keys that no row of the CTA sees have zero codes and lg2 vs =
 // -inf, so no stale byte enters a sum.
@@ -48,10 +49,10 @@ using namespace sm100;
 constexpr int kThreads = 512;
 constexpr int BM = 128;                 // rows of a row tile
 constexpr int BN = 128;                 // tokens of a key tile
-// Register split (setmaxnreg): 256 x 184 + 128 x 104 + 128 x 40 = 65536, what 512
-// threads at 128 each are launched with (checked before the first launch).
-constexpr int kSoftRegs = 184, kConvRegs = 104, kMmaRegs = 40;
-constexpr int kSplitRegs = 256 * kSoftRegs + 128 * kConvRegs + 128 * kMmaRegs;
+// Register split (setmaxnreg): 256 x 168 + 256 x 88 = 65536, what 512 threads at
+// 128 each are launched with (checked before the first launch).
+constexpr int kSoftRegs = 168, kConvRegs = 88;
+constexpr int kSplitRegs = 256 * kSoftRegs + 256 * kConvRegs;
 static_assert(kSplitRegs <= 65536, "register file");
 constexpr float kLazy = 8.0f;           // how far y may pass its reference (log2)
 constexpr float kMinVs = 0x1p-100f;
@@ -63,7 +64,7 @@ struct Lay {
   static constexpr uint32_t kQ = 0, kK = 2 * kTile, kV = 4 * kTile, kSc = 6 * kTile;
   static constexpr uint32_t kScSlot = 3 * BN * 4;       // cs, lv, iv of a tile
   static constexpr uint32_t kBar = kSc + 4 * kScSlot;
-  static constexpr uint32_t kNumBars = 4 + 8 + 6 + 1;
+  static constexpr uint32_t kNumBars = 8 + 4 + 6 + 1 + 2;
   static constexpr uint32_t kTotal = 1024 + kBar + kNumBars * 8 + 16;
   static constexpr uint32_t kS = 0, kO = 2 * BN;        // tensor memory columns
 };
@@ -74,17 +75,15 @@ __device__ __forceinline__ uint32_t sw128(int row, int unit) {
   return (uint32_t)row * 128u + ((uint32_t)(unit ^ (row & 7)) << 4);
 }
 
-// Descriptor of a tile whose reduction runs along its rows: 64 columns (128
-// bytes, 128-byte swizzle) x 8 rows are an atom; the next 8 rows are 1024 bytes
-// on, the next 64 columns a half tile on.
-__device__ __forceinline__ uint64_t desc_rows(uint32_t saddr, uint32_t half_bytes) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
-  d |= (uint64_t)(half_bytes >> 4) << 16;
-  d |= (uint64_t)(1024u >> 4) << 32;
-  d |= (uint64_t)1u << 46;
-  d |= (uint64_t)2u << 61;
-  return d;
+// Descriptors (128-byte swizzle, 8-row groups 1024 bytes apart): the low word
+// has the address and the leading offset, the high word is a constant.  A tile
+// read along its rows (K, Q) needs no leading offset; one whose reduction runs
+// across its rows (V) has 64 columns x 8 rows as its atom, and the next 64
+// columns a half tile on.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t leading) {
+  return ((saddr >> 4) & 0x3FFFu) | (leading >> 4) << 16;
 }
 
 // fp16 x fp16 -> fp32, M = 128; b_rows: B's reduction runs along its rows.
@@ -93,43 +92,47 @@ constexpr uint32_t idesc_f16(int N, bool b_rows) {
          ((uint32_t)(BM >> 4) << 24);
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
                                        uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b),
-      "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b),
+      "r"(idesc), "r"(acc), "r"(kDescHi)
       : "memory");
 }
 
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
                                        uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b),
-      "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b),
+      "r"(idesc), "r"(acc), "r"(kDescHi)
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(
-          taddr),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
-      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
-      "r"(r[30]), "r"(r[31])
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+// tmem_ld32 into part of a longer array.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
+  sm100::tmem_ld32(taddr, *reinterpret_cast<uint32_t(*)[32]>(r));
+}
+
+__device__ __forceinline__ float max3(uint32_t a, uint32_t b, uint32_t c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)),
+      "f"(__uint_as_float(c)));
   return d;
 }
+
 __device__ __forceinline__ float lo2(uint64_t a) { return __uint_as_float((uint32_t)a); }
 __device__ __forceinline__ float hi2(uint64_t a) { return __uint_as_float((uint32_t)(a >> 32)); }
 
@@ -140,15 +143,35 @@ __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t 
                : "memory");
 }
 
-__device__ __forceinline__ void ld_shared2x2(uint32_t addr, uint64_t& a, uint64_t& b) {
-  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr));
+__device__ __forceinline__ void ld_shared4(const float4* p, float (&v)[4]) {
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "r"(smem_u32(p)));
+}
+
+// Scales of a group of 16 tokens: y = c s + lv for a score product s of a row
+// with power rd, and 1 / vs.  c is kept above zero, so that a masked score of
+// -inf stays one (codes under a zero scale are zero, and so are their products).
+__device__ __forceinline__ void group_scales(const float4* sc, float rd, float& c, float& lv,
+                                             float& iv) {
+  const float4 x = *sc;
+  c = fmaxf(x.x * rd, 1e-37f);
+  lv = x.y;
+  iv = x.z;
+}
+
+// y of one token (own scales): c = cs, lv = lg2 vs.
+__device__ __forceinline__ float token_y(uint32_t s, float cs, float rd, float lv) {
+  return fmaf(__uint_as_float(s), fmaxf(cs * rd, 1e-37f), lv);
 }
 
 __device__ __forceinline__ void fence_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-template <int DT, int D>
+// UNI: block_t is a multiple of 16, so that 16 aligned tokens share their scales;
+// the scales of a tile are then eight entries {cs, lg2 vs, 1 / vs, -} and the
+// weights cost half the instructions (prompt of 8192, block_t 64: see launch_dt).
+template <int DT, int D, bool UNI>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_tc_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles) {
   using L = Lay<D>;
@@ -184,16 +207,17 @@ attn_tc_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles) {
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBar);
   uint64_t *k_full = bars, *v_full = bars + 2, *k_empty = bars + 4, *v_empty = bars + 6,
            *sc_full = bars + 8, *s_full = bars + 12, *p_ready = bars + 14, *o_done = bars + 16,
-           *drain = bars + 18;
+           *drain = bars + 18, *q_full = bars + 19;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + L::kNumBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&k_full[i]), 4);
-      mbar_init(smem_u32(&v_full[i]), 4);
+      mbar_init(smem_u32(&v_full[i]), 3);
       mbar_init(smem_u32(&k_empty[i]), 1);
       mbar_init(smem_u32(&v_empty[i]), 1);
+      mbar_init(smem_u32(&q_full[i]), 4);
       mbar_init(smem_u32(&s_full[i]), 1);
       mbar_init(smem_u32(&p_ready[i]), 4);
       mbar_init(smem_u32(&o_done[i]), 1);
@@ -203,86 +227,47 @@ attn_tc_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles) {
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 12) tmem_alloc(smem_u32(tmem_slot), 512);
+  if (warp == 8) tmem_alloc(smem_u32(tmem_slot), 512);
 
-  // queries: a thread per row, scaled by a power of two, fp16, swizzled
-  const int row = R0 + tid;               // of warps 0-7
-  const bool row_on = warp < 8 && row < n_rows;
-  float rd = 1.f;
-  if (warp < 8) {
-    const uint16_t* q = a.q + (int64_t)(s.row0 + (row_on ? row / g : 0)) * a.ldq +
-                        (int64_t)(hk * g + (row_on ? row % g : 0)) * a.hq;
-    const uint32_t dst = sbase + L::kQ + (uint32_t)(tid >> 7) * L::kTile;
-    const bool vec = (reinterpret_cast<uintptr_t>(q) & 15) == 0;
-    float amax = 0.f;
-    uint32_t w[D / 2];
-#pragma unroll
-    for (int u = 0; u < D / 8; ++u) {
-      uint4 x = make_uint4(0u, 0u, 0u, 0u);
-      if (row_on) {
-        if (vec) {
-          x = *reinterpret_cast<const uint4*>(q + 8 * u);
-        } else {
-          const uint16_t* e = q + 8 * u;
-          x = make_uint4(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16,
-                         e[4] | (uint32_t)e[5] << 16, e[6] | (uint32_t)e[7] << 16);
-        }
-      }
-      w[4 * u] = x.x; w[4 * u + 1] = x.y; w[4 * u + 2] = x.z; w[4 * u + 3] = x.w;
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[4 * u + e] << 16)),
-                                 fabsf(__uint_as_float(w[4 * u + e] & 0xFFFF0000u))));
-    }
-    float up;
-    row_power(amax, up, rd);
-#pragma unroll
-    for (int u = 0; u < D / 8; ++u) {
-      uint32_t h[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        h[e] = pack_f16(__uint_as_float(w[4 * u + e] << 16) * up,
-                        __uint_as_float(w[4 * u + e] & 0xFFFF0000u) * up);
-      st_shared16(dst + (uint32_t)(u >> 3) * L::kHalf + sw128(tid & 127, u & 7), h[0], h[1], h[2],
-                  h[3]);
-    }
-    fence_async_shared();
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp >= 12) {
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kConvRegs) : "memory");
+  }
+  if (warp == 12) {
     // ---------------- products ----------------
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kMmaRegs) : "memory");
-    if (warp == 12 && lane == 0 && nt > 0) {
+    if (lane == 0 && nt > 0) {
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity, unsigned site) {
         ok = ok && mbar_wait(smem_u32(bar), parity, abort_flag, a.status, site);
         return ok;
       };
+      // low words of the descriptors; the high word is the same for all
+      const uint32_t qd = desc_lo(sbase + L::kQ, 16), kd = desc_lo(sbase + L::kK, 16),
+                     vd = desc_lo(sbase + L::kV, L::kHalf);
       auto scores = [&](int t, int j) {
-        const uint32_t qa = sbase + L::kQ + (uint32_t)t * L::kTile;
-        const uint32_t ka = sbase + L::kK + (uint32_t)(j & 1) * L::kTile;
+        const uint32_t q = qd + (uint32_t)t * (L::kTile >> 4), k = kd + (uint32_t)(j & 1) * (L::kTile >> 4);
 #pragma unroll
         for (uint32_t h = 0; h < D / 64; ++h)
 #pragma unroll
-          for (uint32_t k = 0; k < 4; ++k)
-            mma_ss(tmem + L::kS + t * BN, smem_desc_k128(qa + h * L::kHalf) + 2ull * k,
-                   smem_desc_k128(ka + h * L::kHalf) + 2ull * k, idesc_f16(BN, false),
-                   (h | k) != 0);
+          for (uint32_t u = 0; u < 4; ++u)
+            mma_ss(tmem + L::kS + t * BN, q + h * (L::kHalf >> 4) + 2 * u,
+                   k + h * (L::kHalf >> 4) + 2 * u, idesc_f16(BN, false), (h | u) != 0);
         mma_commit(smem_u32(&s_full[t]));
       };
       auto values = [&](int t, int j) {
-        const uint32_t va = sbase + L::kV + (uint32_t)(j & 1) * L::kTile;
+        const uint32_t v = vd + (uint32_t)(j & 1) * (L::kTile >> 4);
 #pragma unroll
-        for (uint32_t k = 0; k < BN / 16; ++k)
-          mma_ts(tmem + L::kO + t * D, tmem + L::kS + t * BN + 8 * k,
-                 desc_rows(va + 2048u * k, L::kHalf), idesc_f16(D, true), (j > 0 || k > 0));
+        for (uint32_t u = 0; u < BN / 16; ++u)
+          mma_ts(tmem + L::kO + t * D, tmem + L::kS + t * BN + 8 * u, v + 128u * u,
+                 idesc_f16(D, true), u > 0 || j > 0);
         mma_commit(smem_u32(&o_done[t]));
       };
-      if (wait(&k_full[0], 0, 0x731u)) {
+      if (wait(&k_full[0], 0, 0x731u) && wait(&q_full[0], 0, 0x73Cu) &&
+          (!two || wait(&q_full[1], 0, 0x73Du))) {
         tc_fence_after();
         scores(0, 0);
         if (two) scores(1, 0);
@@ -310,6 +295,7 @@ attn_tc_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles) {
         if (more) mma_commit(smem_u32(&k_empty[(j + 1) & 1]));
       }
       if (!ok) {
+        // products in flight end before the tensor memory is freed
         mma_commit(smem_u32(&drain[0]));
         const uint64_t t0 = globaltimer();
         while (!mbar_try_wait(smem_u32(&drain[0]), 0) && globaltimer() - t0 < 100000000ull) {
@@ -318,105 +304,167 @@ attn_tc_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles) {
     }
     __syncwarp();
   } else if (warp >= 8) {
-    // ---------------- converters ----------------
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kConvRegs) : "memory");
-    constexpr int CH = D / 16;                   // 16-code chunks of a token
-    constexpr int NL = CH;                       // loads of a thread: 128 CH chunks / 128 threads
-    constexpr int TPL = 128 / CH;                // tokens that one load of all threads covers
-    const int ct = tid - 256, ch = ct % CH, tk = ct / CH;
-    const int page = a.c.page, bt = a.c.bt, nblk = page / bt;
-    // pages of the tile's eight groups of 16 tokens, in lanes 0-7
-    auto pages = [&](int t0) -> int {
-      int64_t pg = -1;
-      const int t = t0 + 16 * lane;
-      if (lane < 8 && t < part.hi && t + 16 > all.lo) {
-        pg = kv::page_of(a.b, a.c, b, t);
-        if (pg < 0) record_status(a.status, kStatusBadInput, 0x722u);
-      }
-      return (int)pg;
-    };
-    auto load = [&](uint4 (&x)[NL], const uint8_t* codes, int t0, int pgs) {
+    // ---------------- converters: keys (warps 8-11), values (13-15) ----------------
+    const bool is_k = warp < 12;
+    const uint8_t* codes = is_k ? a.c.k : a.c.v;
+    uint64_t *full = is_k ? k_full : v_full, *empty = is_k ? k_empty : v_empty;
+    const uint32_t dst0 = sbase + (is_k ? L::kK : L::kV);
+    // A tile's eight groups of 16 tokens, each in one page, go round the warps: key
+    // warp w has groups 2 w and 2 w + 1, value warp w groups w, w + 3 and w + 6.  A
+    // lane's 16 codes are chunk lane / 8 of a half row of token lane % 8, so that
+    // eight lanes store one 16-byte unit of eight different rows: no bank conflict.
+    constexpr int GL = D / 32;                   // loads of a lane for a group
+    constexpr int HV = D / 64;                   // half rows
+    const int ch = lane >> 3, w = is_k ? warp & 3 : warp - 13;
+    const int g0 = is_k ? 2 * w : w, gs = is_k ? 1 : 3, ng = is_k || w == 2 ? 2 : 3;
+    const int page = a.c.page, nblk = page / a.c.bt;
+    auto pages = [&](int t0, int (&pg)[3]) {
 #pragma unroll
-      for (int i = 0; i < NL; ++i) {
-        const int tl = i * TPL + tk, t = t0 + tl;
-        const int pg = __shfl_sync(0xffffffffu, pgs, tl >> 4);
-        x[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (pg >= 0 && t >= all.lo && t < part.hi)
-          x[i] = ld_codes16(codes + (((int64_t)pg * a.c.H + hk) * page + t % page) * D + 16 * ch);
+      for (int h = 0; h < 3; ++h) {
+        const int t = t0 + 16 * (g0 + h * gs);
+        pg[h] = -1;
+        if (h < ng && t < part.hi && t + 16 > all.lo) {
+          pg[h] = (int)kv::page_of(a.b, a.c, b, t);
+          if (pg[h] < 0 && lane == 0) record_status(a.status, kStatusBadInput, 0x722u);
+        }
       }
     };
-    auto store = [&](const uint4 (&x)[NL], uint32_t dst) {
+    auto load = [&](uint4 (&x)[3][GL], int t0, const int (&pg)[3]) {
 #pragma unroll
-      for (int i = 0; i < NL; ++i) {
-        const int tl = i * TPL + tk;
-        uint32_t f[8];
+      for (int h = 0; h < 3; ++h) {
+        const int tg = t0 + 16 * (g0 + h * gs);
+        const uint8_t* p =
+            codes + (((int64_t)pg[h] * a.c.H + hk) * page + tg % page + (lane & 7)) * D + 16 * ch;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) codes_to_f16<DT>(word_of(x[i], w), f[2 * w], f[2 * w + 1]);
-        const uint32_t base = dst + (uint32_t)(ch >> 2) * L::kHalf;
-        // lanes of the second half store their units in the other order: no bank conflict
-        const bool odd = (ch >> 2) & 1;
-        const int u = 2 * (ch & 3);
-        st_shared16(base + sw128(tl, odd ? u + 1 : u), odd ? f[4] : f[0], odd ? f[5] : f[1],
-                    odd ? f[6] : f[2], odd ? f[7] : f[3]);
-        st_shared16(base + sw128(tl, odd ? u : u + 1), odd ? f[0] : f[4], odd ? f[1] : f[5],
-                    odd ? f[2] : f[6], odd ? f[3] : f[7]);
+        for (int e = 0; e < GL; ++e) {           // 8 tokens x 64 codes each
+          const int t = tg + (lane & 7) + 8 * (e / HV);
+          x[h][e] = make_uint4(0u, 0u, 0u, 0u);
+          if (pg[h] >= 0 && t >= all.lo && t < part.hi)
+            x[h][e] = ld_codes16(p + 8 * (e / HV) * D + 64 * (e % HV));
+        }
       }
     };
-    // scale of keys and values of token t0 + ct; ok: some row may see it
-    auto scales = [&](int t0, int pgs, float& ks, float& vs) -> bool {
-      const int t = t0 + ct, pg = __shfl_sync(0xffffffffu, pgs, ct >> 4);
-      ks = 0.f;
-      vs = 1.f;
-      if (pg < 0 || t < all.lo || t >= part.hi) return false;
-      const int64_t blk = ((int64_t)pg * a.c.H + hk) * nblk + (t % page) / bt;
-      ks = a.c.ks[blk];
-      vs = a.c.vs[blk];
-      return true;
+    auto store = [&](const uint4 (&x)[3][GL], uint32_t dst) {
+#pragma unroll
+      for (int h = 0; h < 3; ++h) {
+        if (h >= ng) break;
+#pragma unroll
+        for (int e = 0; e < GL; ++e) {
+          uint32_t f[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            codes_to_f16<DT>(word_of(x[h][e], i), f[2 * i], f[2 * i + 1]);
+          const uint32_t base = dst + (uint32_t)(e % HV) * L::kHalf;
+          const int row_ = 16 * (g0 + h * gs) + (lane & 7) + 8 * (e / HV);
+          st_shared16(base + sw128(row_, 2 * ch), f[0], f[1], f[2], f[3]);
+          st_shared16(base + sw128(row_, 2 * ch + 1), f[4], f[5], f[6], f[7]);
+        }
+      }
     };
-    uint4 kx[NL], vx[NL];
+    // scales of token t0 + 32 w + lane (UNI: of its group, whole groups are on)
     float ks = 0.f, vs = 1.f;
     bool on = false;
+    auto scales = [&](int t0, const int (&pg)[3]) {
+      const int t = t0 + 32 * w + lane, p = lane < 16 ? pg[0] : pg[1];
+      on = p >= 0 && (UNI || (t >= all.lo && t < part.hi));
+      ks = 0.f;
+      vs = 1.f;
+      if (on) {
+        const int64_t blk = ((int64_t)p * a.c.H + hk) * nblk + (t % page) / a.c.bt;
+        ks = a.c.ks[blk];
+        vs = a.c.vs[blk];
+      }
+    };
+    uint4 x[3][GL];
+    int pg[3];
     if (nt > 0) {
-      const int pgs = pages(part.lo);
-      load(kx, a.c.k, part.lo, pgs);
-      on = scales(part.lo, pgs, ks, vs);
-      load(vx, a.c.v, part.lo, pgs);
+      pages(part.lo, pg);
+      load(x, part.lo, pg);
+      if (is_k) scales(part.lo, pg);
     }
     for (int j = 0; j < nt; ++j) {
-      const int t1 = part.lo + (j + 1) * BN;
-      const bool more = j + 1 < nt;
-      const int pgs = more ? pages(t1) : -1;
-      const uint32_t parity = ((j >> 1) & 1) ^ 1;
-      if (!warp_wait(smem_u32(&k_empty[j & 1]), parity, abort_flag, a.status, 0x736u)) break;
-      float* sc = reinterpret_cast<float*>(smem + L::kSc + (uint32_t)(j & 3) * L::kScSlot);
-      vs = fmaxf(vs, kMinVs);
-      sc[ct] = ks * (a.scale * kLog2e);
-      sc[BN + ct] = on ? lg2(vs) : -INFINITY;
-      sc[2 * BN + ct] = on ? __fdividef(1.f, vs) : 0.f;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sc_full[j & 3]));
-      store(kx, sbase + L::kK + (uint32_t)(j & 1) * L::kTile);
-      fence_async_shared();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&k_full[j & 1]));
-      if (more) {
-        load(kx, a.c.k, t1, pgs);
-        on = scales(t1, pgs, ks, vs);
+      if (!warp_wait(smem_u32(&empty[j & 1]), ((j >> 1) & 1) ^ 1, abort_flag, a.status, 0x736u))
+        break;
+      if (is_k) {
+        float* sc = reinterpret_cast<float*>(smem + L::kSc + (uint32_t)(j & 3) * L::kScSlot);
+        vs = fmaxf(vs, kMinVs);
+        const float cs = ks * (fabsf(a.scale) * kLog2e);
+        const float lv = on ? lg2(vs) : -INFINITY, iv = on ? __fdividef(1.f, vs) : 0.f;
+        if constexpr (UNI) {
+          if ((lane & 15) == 0)
+            reinterpret_cast<float4*>(sc)[2 * w + (lane >> 4)] = make_float4(cs, lv, iv, 0.f);
+        } else {
+          sc[32 * w + lane] = cs;
+          sc[BN + 32 * w + lane] = lv;
+          sc[2 * BN + 32 * w + lane] = iv;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sc_full[j & 3]));
       }
-      if (!warp_wait(smem_u32(&v_empty[j & 1]), parity, abort_flag, a.status, 0x737u)) break;
-      store(vx, sbase + L::kV + (uint32_t)(j & 1) * L::kTile);
+      const int t1 = part.lo + (j + 1) * BN;
+      if (j + 1 < nt) pages(t1, pg);              // the next tile's pages, then its codes
+      store(x, dst0 + (uint32_t)(j & 1) * L::kTile);
       fence_async_shared();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&v_full[j & 1]));
-      if (more) load(vx, a.c.v, t1, pgs);
+      if (lane == 0) mbar_arrive(smem_u32(&full[j & 1]));
+      if (j + 1 < nt) {
+        load(x, t1, pg);
+        if (is_k) scales(t1, pg);
+      }
     }
-  } else {
+  } else if (warp < 8) {
     // ---------------- softmax ----------------
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftRegs) : "memory");
     const int t = warp >> 2;
     const uint32_t quad = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t st = tmem + quad + L::kS + t * BN, ot = tmem + quad + L::kO + t * D;
     const bool idle = t == 1 && !two;
+    // queries: a thread per row, scaled by a power of two, fp16, swizzled
+    const int row = R0 + tid;
+    const bool row_on = row < n_rows;
+    float rd = 1.f;
+    if (!idle) {
+      const uint16_t* q = a.q + (int64_t)(s.row0 + (row_on ? row / g : 0)) * a.ldq +
+                          (int64_t)(hk * g + (row_on ? row % g : 0)) * a.hq;
+      const uint32_t dst = sbase + L::kQ + (uint32_t)(tid >> 7) * L::kTile;
+      const bool vec = (reinterpret_cast<uintptr_t>(q) & 15) == 0;
+      float amax = 0.f;
+      uint32_t w[D / 2];
+#pragma unroll
+      for (int u = 0; u < D / 8; ++u) {
+        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        if (row_on) {
+          if (vec) {
+            x = *reinterpret_cast<const uint4*>(q + 8 * u);
+          } else {
+            const uint16_t* e = q + 8 * u;
+            x = make_uint4(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16,
+                           e[4] | (uint32_t)e[5] << 16, e[6] | (uint32_t)e[7] << 16);
+          }
+        }
+        w[4 * u] = x.x; w[4 * u + 1] = x.y; w[4 * u + 2] = x.z; w[4 * u + 3] = x.w;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[4 * u + e] << 16)),
+                                   fabsf(__uint_as_float(w[4 * u + e] & 0xFFFF0000u))));
+      }
+      float up;
+      row_power(amax, up, rd);
+      if (a.scale < 0.f) up = -up;          // scores then only take the scale's magnitude
+#pragma unroll
+      for (int u = 0; u < D / 8; ++u) {
+        uint32_t h[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          h[e] = pack_f16(__uint_as_float(w[4 * u + e] << 16) * up,
+                          __uint_as_float(w[4 * u + e] & 0xFFFF0000u) * up);
+        st_shared16(dst + (uint32_t)(u >> 3) * L::kHalf + sw128(tid & 127, u & 7), h[0], h[1], h[2],
+                    h[3]);
+      }
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&q_full[t]));
+    }
     int row_lo = 0, row_hi = 0, in_lo, in_hi, unused;
     if (row_on) row_range(a, s, row / g, row_lo, row_hi);
     // tokens that every row of this row tile sees
@@ -424,7 +472,6 @@ attn_tc_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles) {
     row_range(a, s, i1, in_lo, unused);
     row_range(a, s, i0, unused, in_hi);
     float mo = -INFINITY, l = 0.f;
-    const uint64_t rd2 = pack2(rd, rd);
     bool ok = true;
     for (int j = 0; j < nt && !idle; ++j) {
       const int t0 = part.lo + j * BN;
@@ -432,36 +479,50 @@ attn_tc_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles) {
            warp_wait(smem_u32(&s_full[t]), j & 1, abort_flag, a.status, 0x739u);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t sc = sbase + L::kSc + (uint32_t)(j & 3) * L::kScSlot;
-      uint64_t y[BN / 2];
-      float mx = -INFINITY;
-      {
-        uint32_t r[2][32];               // two chunks of 32 scores in flight
-        tmem_ld32(st, r[0]);
+      const float4* sc4 =
+          reinterpret_cast<const float4*>(smem + L::kSc + (uint32_t)(j & 3) * L::kScSlot);
+      const bool masked = t0 < in_lo || t0 + BN > in_hi;
+      const int a0 = row_lo - t0, a1 = row_hi - t0;
+      // all scores at once: a load's latency is near that of a whole row
+      uint32_t y[BN];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          tmem_ld_wait();
-          if (q < 3) tmem_ld32(st + 32 * (q + 1), r[(q + 1) & 1]);
+      for (int q = 0; q < BN / 32; ++q) tmem_ld32(st + 32 * q, y + 32 * q);
+      tmem_ld_wait();
+      if constexpr (!UNI) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            uint64_t c0, c1, v0, v1;
-            ld_shared2x2(sc + 128 * q + 16 * i, c0, c1);
-            ld_shared2x2(sc + 4 * BN + 128 * q + 16 * i, v0, v1);
-            const uint32_t* w = &r[q & 1][4 * i];
-            y[16 * q + 2 * i] = fma2(mul2((uint64_t)w[1] << 32 | w[0], c0), rd2, v0);
-            y[16 * q + 2 * i + 1] = fma2(mul2((uint64_t)w[3] << 32 | w[2], c1), rd2, v1);
-          }
+        for (int i = 0; i < BN / 4; ++i) {
+          float c[4], v[4];
+          ld_shared4(sc4 + i, c);
+          ld_shared4(sc4 + BN / 4 + i, v);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            y[4 * i + e] = __float_as_uint(token_y(y[4 * i + e], c[e], rd, v[e]));
         }
       }
-      if (t0 < in_lo || t0 + BN > in_hi) {
-        const int a0 = row_lo - t0, a1 = row_hi - t0;
+      if (masked) {                        // -inf outside the row's range
 #pragma unroll
-        for (int i = 0; i < BN / 2; ++i)
-          y[i] = pack2(2 * i >= a0 && 2 * i < a1 ? lo2(y[i]) : -INFINITY,
-                       2 * i + 1 >= a0 && 2 * i + 1 < a1 ? hi2(y[i]) : -INFINITY);
+        for (int i = 0; i < BN; ++i)
+          if (i < a0 || i >= a1) y[i] = 0xFF800000u;
       }
+      float mx = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < BN / 2; ++i) mx = fmaxf(mx, fmaxf(lo2(y[i]), hi2(y[i])));
+      for (int q = 0; q < BN / 16; ++q) {
+        float m0 = max3(y[16 * q], y[16 * q + 1], y[16 * q + 2]);
+        float m1 = max3(y[16 * q + 3], y[16 * q + 4], y[16 * q + 5]);
+#pragma unroll
+        for (int i = 6; i < 14; i += 4) {
+          m0 = max3(__float_as_uint(m0), y[16 * q + i], y[16 * q + i + 1]);
+          m1 = max3(__float_as_uint(m1), y[16 * q + i + 2], y[16 * q + i + 3]);
+        }
+        m0 = max3(__float_as_uint(m0), y[16 * q + 14], y[16 * q + 15]);
+        if constexpr (UNI) {
+          float c, lv, iv;
+          group_scales(sc4 + q, rd, c, lv, iv);
+          mx = fmaxf(mx, fmaf(c, fmaxf(m0, m1), lv));
+        } else {
+          mx = max3(__float_as_uint(mx), __float_as_uint(m0), __float_as_uint(m1));
+        }
+      }
       const bool up = mx > mo + kLazy || (mo == -INFINITY && mx != -INFINITY);
       if (__any_sync(0xffffffffu, up)) {
         const float f = up ? ex2(mo - mx) : 1.f;     // 0 for the first keys seen
@@ -473,37 +534,54 @@ attn_tc_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles) {
             break;
           }
           tc_fence_after();
-#pragma unroll
-          for (int q = 0; q < D / 32; ++q) {
-            uint32_t r[32];
-            tmem_ld32(ot + 32 * q, r);
+#pragma unroll 1
+          for (int q = 0; q < D / 16; ++q) {
+            uint32_t r[16];
+            tmem_ld16(ot + 16 * q, r);
             tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
-            tmem_st32(ot + 32 * q, r);
+            for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
+            tmem_st16(ot + 16 * q, r);
           }
         }
       }
       const float neg = -finite(mo);
-      const uint64_t neg2 = pack2(neg, neg);
-      uint64_t l2 = pack2(l, 0.f);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t p[32];
+      for (int h = 0; h < BN / 32; ++h) {
+        uint32_t p[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          uint64_t v0, v1;
-          ld_shared2x2(sc + 8 * BN + 256 * h + 16 * i, v0, v1);
-          const uint64_t d0 = add2(y[32 * h + 2 * i], neg2), d1 = add2(y[32 * h + 2 * i + 1], neg2);
-          const float p0 = ex2(lo2(d0)), p1 = ex2(hi2(d0)), p2 = ex2(lo2(d1)), p3 = ex2(hi2(d1));
-          l2 = fma2(pack2(p0, p1), v0, l2);
-          l2 = fma2(pack2(p2, p3), v1, l2);
-          p[2 * i] = pack_f16(p0, p1);
-          p[2 * i + 1] = pack_f16(p2, p3);
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t* w = y + 32 * h + 16 * u;
+          if constexpr (UNI) {
+            float c, lv, iv;
+            group_scales(sc4 + 2 * h + u, rd, c, lv, iv);
+            const uint64_t c2 = pack2(c, c), b2 = pack2(lv + neg, lv + neg);
+            uint64_t sum = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint64_t d = fma2((uint64_t)w[2 * i + 1] << 32 | w[2 * i], c2, b2);
+              const float p0 = ex2(lo2(d)), p1 = ex2(hi2(d));
+              sum = add2(sum, pack2(p0, p1));
+              p[8 * u + i] = pack_f16(p0, p1);
+            }
+            l = fmaf(lo2(sum) + hi2(sum), iv, l);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float iv[4], x[4];
+              ld_shared4(sc4 + BN / 2 + 8 * h + 4 * u + i, iv);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                x[e] = ex2(__uint_as_float(w[4 * i + e]) + neg);
+                l = fmaf(x[e], iv[e], l);
+              }
+              p[8 * u + 2 * i] = pack_f16(x[0], x[1]);
+              p[8 * u + 2 * i + 1] = pack_f16(x[2], x[3]);
+            }
+          }
         }
-        tmem_st32(st + 32 * h, p);
+        tmem_st16(st + 16 * h, p);
       }
-      l = lo2(l2) + hi2(l2);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -569,15 +647,15 @@ attn_tc_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles) {
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == 8) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
 }
 
-template <int DT, int D>
+template <int DT, int D, bool UNI>
 cudaError_t launch_t(const AttnArgs& a, const AttnParts& p, cudaStream_t st) {
-  auto kern = attn_tc_kernel<DT, D>;
+  auto kern = attn_tc_kernel<DT, D, UNI>;
   static bool ready[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -611,6 +689,14 @@ cudaError_t launch_t(const AttnArgs& a, const AttnParts& p, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, kern, a, p, (int)tiles);
 }
 
+template <int DT>
+cudaError_t launch_dt(const AttnArgs& a, const AttnParts& p, cudaStream_t st) {
+  const bool uni = a.c.bt % 16 == 0;
+  if (a.c.D == 64)
+    return uni ? launch_t<DT, 64, true>(a, p, st) : launch_t<DT, 64, false>(a, p, st);
+  return uni ? launch_t<DT, 128, true>(a, p, st) : launch_t<DT, 128, false>(a, p, st);
+}
+
 }  // namespace
 
 int64_t attn_tc_tiles(int64_t max_q, int64_t group) {
@@ -627,9 +713,7 @@ int attn_tc_splits(int64_t B, int64_t Hkv, int64_t max_q, int64_t group, int64_t
 }
 
 cudaError_t launch_attn_tc(const AttnArgs& a, const AttnParts& p, cudaStream_t st) {
-  if (a.c.dtype == kInt8)
-    return a.c.D == 64 ? launch_t<kInt8, 64>(a, p, st) : launch_t<kInt8, 128>(a, p, st);
-  return a.c.D == 64 ? launch_t<kFp8, 64>(a, p, st) : launch_t<kFp8, 128>(a, p, st);
+  return a.c.dtype == kInt8 ? launch_dt<kInt8>(a, p, st) : launch_dt<kFp8>(a, p, st);
 }
 
 }  // namespace bq
