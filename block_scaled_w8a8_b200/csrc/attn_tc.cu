@@ -13,9 +13,11 @@
 //   warp 12         issues the products: S_a = Q_a K^T (both operands in shared
 //                   memory) and O_a += P_a V (P_a from tensor memory, V as it
 //                   lies, its rows running along the reduction).
-// The issue order O_0(j), S_0(j+1), O_1(j), S_1(j+1) keeps the tensor cores on
-// one row tile while the other's softmax runs.
-// Tensor memory: S_0, S_1 (128 columns each, P_a in the first 64 of S_a), O_0, O_1.
+// Scores are formed 64 keys at a time and each row tile has two such blocks, so
+// that the next block's scores and the last one's value product run on the
+// tensor cores while a block is in the softmax: neither waits for the other.
+// Tensor memory: four score blocks of 64 columns (the weights in the first 32 of
+// each), O_0, O_1.
 //
 // Weights: with y = z + lg2 vs (z the score in log2 units, vs the value's block
 // scale) and mo a reference of the row, the weight is 2^(y - mo), so the product
@@ -49,9 +51,10 @@ using namespace sm100;
 constexpr int kThreads = 512;
 constexpr int BM = 128;                 // rows of a row tile
 constexpr int BN = 128;                 // tokens of a key tile
-// Register split (setmaxnreg): 256 x 168 + 256 x 88 = 65536, what 512 threads at
+constexpr int SN = 64;                  // tokens of a score block
+// Register split (setmaxnreg): 256 x 152 + 256 x 104 = 65536, what 512 threads at
 // 128 each are launched with (checked before the first launch).
-constexpr int kSoftRegs = 168, kConvRegs = 88;
+constexpr int kSoftRegs = 152, kConvRegs = 104;
 constexpr int kSplitRegs = 256 * kSoftRegs + 256 * kConvRegs;
 static_assert(kSplitRegs <= 65536, "register file");
 constexpr float kLazy = 8.0f;           // how far y may pass its reference (log2)
@@ -64,7 +67,7 @@ struct Lay {
   static constexpr uint32_t kQ = 0, kK = 2 * kTile, kV = 4 * kTile, kSc = 6 * kTile;
   static constexpr uint32_t kScSlot = 3 * BN * 4;       // cs, lv, iv of a tile
   static constexpr uint32_t kBar = kSc + 4 * kScSlot;
-  static constexpr uint32_t kNumBars = 8 + 4 + 6 + 1 + 2;
+  static constexpr uint32_t kNumBars = 8 + 4 + 10 + 1 + 4;
   static constexpr uint32_t kTotal = 1024 + kBar + kNumBars * 8 + 16;
   static constexpr uint32_t kS = 0, kO = 2 * BN;        // tensor memory columns
 };
@@ -92,23 +95,38 @@ constexpr uint32_t idesc_f16(int N, bool b_rows) {
          ((uint32_t)(BM >> 4) << 24);
 }
 
+// The products are issued by a whole warp in step, one lane (`on`) doing it, so
+// that descriptors and addresses stay in uniform registers: under a divergent
+// branch every operand is moved there anew, 80 cycles an instruction, more than
+// the product itself takes.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
-                                       uint32_t acc) {
+                                       uint32_t acc, uint32_t on) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 e, %6, 0;\n\t"
       "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b),
-      "r"(idesc), "r"(acc), "r"(kDescHi)
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b),
+      "r"(idesc), "r"(acc), "r"(kDescHi), "r"(on)
       : "memory");
 }
 
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
-                                       uint32_t acc) {
+                                       uint32_t acc, uint32_t on) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 e, %6, 0;\n\t"
       "mov.b64 y, {%2, %5};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b),
-      "r"(idesc), "r"(acc), "r"(kDescHi)
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d), "r"(a),
+      "r"(b), "r"(idesc), "r"(acc), "r"(kDescHi), "r"(on)
+      : "memory");
+}
+
+__device__ __forceinline__ void commit_if(uint32_t bar, uint32_t on) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          bar),
+      "r"(on)
       : "memory");
 }
 
@@ -135,6 +153,17 @@ __device__ __forceinline__ float max3(uint32_t a, uint32_t b, uint32_t c) {
 
 __device__ __forceinline__ float lo2(uint64_t a) { return __uint_as_float((uint32_t)a); }
 __device__ __forceinline__ float hi2(uint64_t a) { return __uint_as_float((uint32_t)(a >> 32)); }
+
+// warp_wait, with the clock of its bound left alone while the wait is an ordinary
+// one: reading %globaltimer costs more than most waits here last.
+__device__ __forceinline__ bool wait_bar(const uint64_t* bar, uint32_t parity,
+                                         volatile int* abort_flag, unsigned* status,
+                                         unsigned site) {
+  const uint32_t b = smem_u32(bar);
+  for (int i = 0; i < 64; ++i)
+    if (__all_sync(0xffffffffu, mbar_try_wait(b, parity))) return true;
+  return warp_wait(b, parity, abort_flag, status, site);
+}
 
 __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
                                             uint32_t d) {
@@ -178,7 +207,8 @@ attn_tc_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles) {
   extern __shared__ uint8_t smem_raw[];
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);    // known to be uniform
   // the tiles with the most keys first: later rows see more
   int idx = blockIdx.x;
   const int hk = idx % a.c.H;
@@ -199,15 +229,16 @@ attn_tc_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles) {
   const int i_lo = R0 / g, i_hi = min(s.n - 1, (R0 + 2 * BM - 1) / g);
   const Range all = tile_range(a, s, i_lo, i_hi);
   const Range part = split_range(all, split, parts.splits, BN);
-  const int nt = part.hi > part.lo ? (part.hi - part.lo + BN - 1) / BN : 0;
+  const int keys = max(part.hi - part.lo, 0);
+  const int nt = (keys + BN - 1) / BN, nb = (keys + SN - 1) / SN;   // key tiles, score blocks
 
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBar);
   uint64_t *k_full = bars, *v_full = bars + 2, *k_empty = bars + 4, *v_empty = bars + 6,
-           *sc_full = bars + 8, *s_full = bars + 12, *p_ready = bars + 14, *o_done = bars + 16,
-           *drain = bars + 18, *q_full = bars + 19;
+           *sc_full = bars + 8, *s_full = bars + 12, *p_ready = bars + 16, *o_done = bars + 20,
+           *drain = bars + 22, *q_full = bars + 23, *o_last = bars + 25;   // s_full, p_ready: [row tile][block & 1]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + L::kNumBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -218,11 +249,14 @@ attn_tc_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles) {
       mbar_init(smem_u32(&k_empty[i]), 1);
       mbar_init(smem_u32(&v_empty[i]), 1);
       mbar_init(smem_u32(&q_full[i]), 4);
-      mbar_init(smem_u32(&s_full[i]), 1);
-      mbar_init(smem_u32(&p_ready[i]), 4);
+      mbar_init(smem_u32(&o_last[i]), 1);
       mbar_init(smem_u32(&o_done[i]), 1);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&sc_full[i]), 4);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(smem_u32(&sc_full[i]), 4);
+      mbar_init(smem_u32(&s_full[i]), 1);
+      mbar_init(smem_u32(&p_ready[i]), 4);
+    }
     mbar_init(smem_u32(&drain[0]), 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -239,70 +273,70 @@ attn_tc_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles) {
   }
   if (warp == 12) {
     // ---------------- products ----------------
-    if (lane == 0 && nt > 0) {
-      bool ok = true;
-      auto wait = [&](uint64_t* bar, uint32_t parity, unsigned site) {
-        ok = ok && mbar_wait(smem_u32(bar), parity, abort_flag, a.status, site);
-        return ok;
-      };
-      // low words of the descriptors; the high word is the same for all
-      const uint32_t qd = desc_lo(sbase + L::kQ, 16), kd = desc_lo(sbase + L::kK, 16),
-                     vd = desc_lo(sbase + L::kV, L::kHalf);
-      auto scores = [&](int t, int j) {
-        const uint32_t q = qd + (uint32_t)t * (L::kTile >> 4), k = kd + (uint32_t)(j & 1) * (L::kTile >> 4);
+    const int n = __shfl_sync(0xffffffffu, nb, 0);
+    const bool both = __shfl_sync(0xffffffffu, two ? 1 : 0, 0) != 0;
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), on = elect_one();
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity, unsigned site) {
+      ok = ok && wait_bar(bar, parity, abort_flag, a.status, site);
+      return ok;
+    };
+    // low words of the descriptors; the high word is the same for all
+    const uint32_t qd = desc_lo(sbase + L::kQ, 16), kd = desc_lo(sbase + L::kK, 16),
+                   vd = desc_lo(sbase + L::kV, L::kHalf);
+    auto scores = [&](int t, int i) {                // block i
+      const uint32_t q = qd + (uint32_t)t * (L::kTile >> 4);
+      const uint32_t k = kd + (uint32_t)((i >> 1) & 1) * (L::kTile >> 4) +
+                         (uint32_t)(i & 1) * (SN * 128 >> 4);
 #pragma unroll
-        for (uint32_t h = 0; h < D / 64; ++h)
+      for (uint32_t h = 0; h < D / 64; ++h)
 #pragma unroll
-          for (uint32_t u = 0; u < 4; ++u)
-            mma_ss(tmem + L::kS + t * BN, q + h * (L::kHalf >> 4) + 2 * u,
-                   k + h * (L::kHalf >> 4) + 2 * u, idesc_f16(BN, false), (h | u) != 0);
-        mma_commit(smem_u32(&s_full[t]));
-      };
-      auto values = [&](int t, int j) {
-        const uint32_t v = vd + (uint32_t)(j & 1) * (L::kTile >> 4);
+        for (uint32_t u = 0; u < 4; ++u)
+          mma_ss(tm + L::kS + 2 * SN * t + SN * (i & 1), q + h * (L::kHalf >> 4) + 2 * u,
+                 k + h * (L::kHalf >> 4) + 2 * u, idesc_f16(SN, false), (h | u) != 0, on);
+      commit_if(smem_u32(&s_full[2 * t + (i & 1)]), on);
+    };
+    auto values = [&](int t, int i) {
+      const uint32_t v = vd + (uint32_t)((i >> 1) & 1) * (L::kTile >> 4) +
+                         (uint32_t)(i & 1) * (SN * 128 >> 4);
 #pragma unroll
-        for (uint32_t u = 0; u < BN / 16; ++u)
-          mma_ts(tmem + L::kO + t * D, tmem + L::kS + t * BN + 8 * u, v + 128u * u,
-                 idesc_f16(D, true), u > 0 || j > 0);
-        mma_commit(smem_u32(&o_done[t]));
-      };
-      if (wait(&k_full[0], 0, 0x731u) && wait(&q_full[0], 0, 0x73Cu) &&
-          (!two || wait(&q_full[1], 0, 0x73Du))) {
+      for (uint32_t u = 0; u < SN / 16; ++u)
+        mma_ts(tm + L::kO + t * D, tm + L::kS + 2 * SN * t + SN * (i & 1) + 8 * u, v + 128u * u,
+               idesc_f16(D, true), u > 0 || i > 0, on);
+      commit_if(smem_u32(i == n - 1 ? &o_last[t] : &o_done[t]), on);
+    };
+    // a block's score buffer is free once the block two before it has been
+    // through the value product, which is issued ahead of it
+    auto next_scores = [&](int i) {
+      if ((i & 1) == 0 && !wait(&k_full[(i >> 1) & 1], (i >> 2) & 1, 0x731u)) return;
+      tc_fence_after();
+      scores(0, i);
+      if (both) scores(1, i);
+      if ((i & 1) || i == n - 1) commit_if(smem_u32(&k_empty[(i >> 1) & 1]), on);
+    };
+    if (n > 0 && wait(&q_full[0], 0, 0x73Cu) && (!both || wait(&q_full[1], 0, 0x73Du)))
+      next_scores(0);
+    for (int i = 0; i < n && ok; ++i) {
+      if (i + 1 < n) next_scores(i + 1);
+      if ((i & 1) == 0) wait(&v_full[(i >> 1) & 1], (i >> 2) & 1, 0x732u);
+      if (!wait(&p_ready[i & 1], (i >> 1) & 1, 0x733u)) break;
+      tc_fence_after();
+      values(0, i);
+      if (both) {
+        if (!wait(&p_ready[2 + (i & 1)], (i >> 1) & 1, 0x735u)) break;
         tc_fence_after();
-        scores(0, 0);
-        if (two) scores(1, 0);
-        mma_commit(smem_u32(&k_empty[0]));
+        values(1, i);
       }
-      for (int j = 0; j < nt && ok; ++j) {
-        const bool more = j + 1 < nt;
-        if (!wait(&v_full[j & 1], (j >> 1) & 1, 0x732u)) break;
-        if (!wait(&p_ready[0], j & 1, 0x733u)) break;
-        tc_fence_after();
-        values(0, j);
-        if (!two) mma_commit(smem_u32(&v_empty[j & 1]));
-        if (more) {
-          if (!wait(&k_full[(j + 1) & 1], ((j + 1) >> 1) & 1, 0x734u)) break;
-          tc_fence_after();
-          scores(0, j + 1);
-        }
-        if (two) {
-          if (!wait(&p_ready[1], j & 1, 0x735u)) break;
-          tc_fence_after();
-          values(1, j);
-          mma_commit(smem_u32(&v_empty[j & 1]));
-          if (more) scores(1, j + 1);
-        }
-        if (more) mma_commit(smem_u32(&k_empty[(j + 1) & 1]));
-      }
-      if (!ok) {
-        // products in flight end before the tensor memory is freed
-        mma_commit(smem_u32(&drain[0]));
-        const uint64_t t0 = globaltimer();
-        while (!mbar_try_wait(smem_u32(&drain[0]), 0) && globaltimer() - t0 < 100000000ull) {
-        }
-      }
+      if ((i & 1) || i == n - 1) commit_if(smem_u32(&v_empty[(i >> 1) & 1]), on);
     }
-    __syncwarp();
+    if (!ok) {
+      // products in flight end before the tensor memory is freed
+      commit_if(smem_u32(&drain[0]), on);
+      const uint64_t t0 = globaltimer();
+      while (!mbar_try_wait(smem_u32(&drain[0]), 0) && globaltimer() - t0 < 100000000ull) {
+      }
+      __syncwarp();
+    }
   } else if (warp >= 8) {
     // ---------------- converters: keys (warps 8-11), values (13-15) ----------------
     const bool is_k = warp < 12;
@@ -383,7 +417,7 @@ attn_tc_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles) {
       if (is_k) scales(part.lo, pg);
     }
     for (int j = 0; j < nt; ++j) {
-      if (!warp_wait(smem_u32(&empty[j & 1]), ((j >> 1) & 1) ^ 1, abort_flag, a.status, 0x736u))
+      if (!wait_bar(&empty[j & 1], ((j >> 1) & 1) ^ 1, abort_flag, a.status, 0x736u))
         break;
       if (is_k) {
         float* sc = reinterpret_cast<float*>(smem + L::kSc + (uint32_t)(j & 3) * L::kScSlot);
@@ -417,7 +451,7 @@ attn_tc_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftRegs) : "memory");
     const int t = warp >> 2;
     const uint32_t quad = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t st = tmem + quad + L::kS + t * BN, ot = tmem + quad + L::kO + t * D;
+    const uint32_t ot = tmem + quad + L::kO + t * D;
     const bool idle = t == 1 && !two;
     // queries: a thread per row, scaled by a power of two, fp16, swizzled
     const int row = R0 + tid;
@@ -473,40 +507,44 @@ attn_tc_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles) {
     row_range(a, s, i0, unused, in_hi);
     float mo = -INFINITY, l = 0.f;
     bool ok = true;
-    for (int j = 0; j < nt && !idle; ++j) {
-      const int t0 = part.lo + j * BN;
-      ok = warp_wait(smem_u32(&sc_full[j & 3]), (j >> 2) & 1, abort_flag, a.status, 0x738u) &&
-           warp_wait(smem_u32(&s_full[t]), j & 1, abort_flag, a.status, 0x739u);
+    for (int i = 0; i < nb && !idle; ++i) {
+      const int t0 = part.lo + i * SN, j = i >> 1;       // block i of tile j
+      const uint32_t st = tmem + quad + L::kS + 2 * SN * t + SN * (i & 1);
+      ok = ((i & 1) ||
+            wait_bar(&sc_full[j & 3], (j >> 2) & 1, abort_flag, a.status, 0x738u)) &&
+           wait_bar(&s_full[2 * t + (i & 1)], j & 1, abort_flag, a.status, 0x739u);
       if (!ok) break;
       tc_fence_after();
+      // UNI: the block's four groups; otherwise its 64 entries of each of three arrays
       const float4* sc4 =
-          reinterpret_cast<const float4*>(smem + L::kSc + (uint32_t)(j & 3) * L::kScSlot);
-      const bool masked = t0 < in_lo || t0 + BN > in_hi;
+          reinterpret_cast<const float4*>(smem + L::kSc + (uint32_t)(j & 3) * L::kScSlot) +
+          (UNI ? 4 : SN / 4) * (i & 1);
+      const bool masked = t0 < in_lo || t0 + SN > in_hi;
       const int a0 = row_lo - t0, a1 = row_hi - t0;
       // all scores at once: a load's latency is near that of a whole row
-      uint32_t y[BN];
+      uint32_t y[SN];
 #pragma unroll
-      for (int q = 0; q < BN / 32; ++q) tmem_ld32(st + 32 * q, y + 32 * q);
+      for (int q = 0; q < SN / 32; ++q) tmem_ld32(st + 32 * q, y + 32 * q);
       tmem_ld_wait();
       if constexpr (!UNI) {
 #pragma unroll
-        for (int i = 0; i < BN / 4; ++i) {
+        for (int e4 = 0; e4 < SN / 4; ++e4) {
           float c[4], v[4];
-          ld_shared4(sc4 + i, c);
-          ld_shared4(sc4 + BN / 4 + i, v);
+          ld_shared4(sc4 + e4, c);
+          ld_shared4(sc4 + BN / 4 + e4, v);
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            y[4 * i + e] = __float_as_uint(token_y(y[4 * i + e], c[e], rd, v[e]));
+            y[4 * e4 + e] = __float_as_uint(token_y(y[4 * e4 + e], c[e], rd, v[e]));
         }
       }
       if (masked) {                        // -inf outside the row's range
 #pragma unroll
-        for (int i = 0; i < BN; ++i)
+        for (int i = 0; i < SN; ++i)
           if (i < a0 || i >= a1) y[i] = 0xFF800000u;
       }
       float mx = -INFINITY;
 #pragma unroll
-      for (int q = 0; q < BN / 16; ++q) {
+      for (int q = 0; q < SN / 16; ++q) {
         float m0 = max3(y[16 * q], y[16 * q + 1], y[16 * q + 2]);
         float m1 = max3(y[16 * q + 3], y[16 * q + 4], y[16 * q + 5]);
 #pragma unroll
@@ -528,8 +566,8 @@ attn_tc_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles) {
         const float f = up ? ex2(mo - mx) : 1.f;     // 0 for the first keys seen
         if (up) mo = mx;
         l *= f;
-        if (j > 0) {
-          if (!warp_wait(smem_u32(&o_done[t]), (j - 1) & 1, abort_flag, a.status, 0x73Au)) {
+        if (i > 0) {
+          if (!wait_bar(&o_done[t], (i - 1) & 1, abort_flag, a.status, 0x73Au)) {
             ok = false;
             break;
           }
@@ -547,7 +585,7 @@ attn_tc_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles) {
       }
       const float neg = -finite(mo);
 #pragma unroll
-      for (int h = 0; h < BN / 32; ++h) {
+      for (int h = 0; h < SN / 32; ++h) {
         uint32_t p[16];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
@@ -585,10 +623,10 @@ attn_tc_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles) {
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&p_ready[t]));
+      if (lane == 0) mbar_arrive(smem_u32(&p_ready[2 * t + (i & 1)]));
     }
     if (nt > 0 && !idle && ok)
-      ok = warp_wait(smem_u32(&o_done[t]), (nt - 1) & 1, abort_flag, a.status, 0x73Bu);
+      ok = wait_bar(&o_last[t], 0, abort_flag, a.status, 0x73Bu);
     if (ok && !idle) {
       tc_fence_after();
       const int64_t tok = s.row0 + (row_on ? row / g : 0);
