@@ -36,6 +36,39 @@ __device__ __forceinline__ int64_t mx_sf_index(int64_t r, int64_t g, int64_t K) 
   return ((r / 128) * (K / 128) + g / 4) * 512 + 16 * (r % 32) + 4 * ((r % 128) / 32) + g % 4;
 }
 
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// y of eight elements: r, w as packed bf16.
+__device__ __forceinline__ void normed(const uint4& r, const uint4& w, float rstd, float w_off,
+                                       float (&y)[8]) {
+  const uint32_t rr[4] = {r.x, r.y, r.z, r.w}, ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    y[2 * e] = __uint_as_float(rr[e] << 16) * rstd * (__uint_as_float(ww[e] << 16) + w_off);
+    y[2 * e + 1] = __uint_as_float(rr[e] & 0xFFFF0000u) * rstd *
+                   (__uint_as_float(ww[e] & 0xFFFF0000u) + w_off);
+  }
+}
+
+// Four codes of y * inv, |y * inv| <= 127 (1 + 2^-22).
+__device__ __forceinline__ uint32_t int8x4(const float* y, float inv) {
+  uint32_t b[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) b[e] = __float_as_uint(fmaf(y[e], inv, 12582912.0f));
+  return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+}
+
+__device__ __forceinline__ uint32_t e4m3x4(const float* y, float inv) {
+  unsigned short lo, hi;     // the first source operand lands in the upper byte
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(y[1] * inv), "f"(y[0] * inv));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(y[3] * inv), "f"(y[2] * inv));
+  return (uint32_t)lo | (uint32_t)hi << 16;
+}
+
 // Any width, group, stride and alignment: a CTA per row, the row's r in shared
 // memory as bf16 (exactly what res_out holds), a warp per group.
 template <int DT>
@@ -94,6 +127,158 @@ __global__ void __launch_bounds__(kAnyThreads) norm_any_kernel(const NormArgs a)
   }
 }
 
+// Rows of whole 16-byte vectors, groups of 8 lanes' worth of a power of two (or
+// the whole row): a CTA per row, V vectors of 8 elements a thread, everything in
+// registers, one barrier a row.  Memory-bound: x and the residual are read once,
+// the sum, the codes and the scales written once.
+//
+// Codes are formed with the reciprocal of the scale: y itself is only good to an
+// fp32 rounding, and one more of those moves a code only where y / s lies within
+// that of a border.  INT8: fma(y, 1/s, 1.5 * 2^23) rounds to nearest even and
+// leaves the code in the low byte, with no conversion unit involved.
+template <int DT, int V>
+__global__ void __launch_bounds__(V == 1 ? 1024 : 512)
+norm_vec_kernel(const NormArgs a, const int lpg) {       // lpg: lanes of a group, 0 = the row
+  __shared__ float red[2][2][32];
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
+  const int nvec = (int)(a.K / 8);
+  const float inv_k = __fdiv_rn(1.0f, (float)a.K);
+  uint4 wv[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int v = i * nt + tid;
+    wv[i] = v < nvec ? __ldg(reinterpret_cast<const uint4*>(a.w) + v) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  int parity = 0;
+  for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x, parity ^= 1) {
+    const uint4* x = reinterpret_cast<const uint4*>(a.x + m * a.ldx);
+    const uint4* res = reinterpret_cast<const uint4*>(a.res + m * a.ldr);
+    uint4 rv[V], sv[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int v = i * nt + tid;
+      rv[i] = sv[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (v < nvec) {
+        rv[i] = x[v];
+        if (a.res) sv[i] = res[v];
+      }
+    }
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      uint32_t* r = reinterpret_cast<uint32_t*>(&rv[i]);
+      const uint32_t* t = reinterpret_cast<const uint32_t*>(&sv[i]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (a.res) {
+          const float lo = __uint_as_float(r[e] << 16) + __uint_as_float(t[e] << 16);
+          const float hi = __uint_as_float(r[e] & 0xFFFF0000u) + __uint_as_float(t[e] & 0xFFFF0000u);
+          r[e] = pack_bf16(lo, hi);
+        }
+        const float lo = __uint_as_float(r[e] << 16), hi = __uint_as_float(r[e] & 0xFFFF0000u);
+        sum = fmaf(lo, lo, fmaf(hi, hi, sum));
+      }
+      const int v = i * nt + tid;
+      if (a.res_out && v < nvec) reinterpret_cast<uint4*>(a.res_out + m * a.ldro)[v] = rv[i];
+    }
+    sum = warp_sum(sum);
+    if (lane == 0) red[parity][0][warp] = sum;
+    __syncthreads();
+    sum = lane < nw ? red[parity][0][lane] : 0.f;
+    sum = warp_sum(sum);
+    const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(fmaf(sum, inv_k, a.eps)));
+    float row_max = 0.f;
+    if (lpg == 0) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        float y[8];
+        normed(rv[i], wv[i], rstd, a.w_off, y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) row_max = fmaxf(row_max, fabsf(y[e]));
+      }
+      row_max = warp_max(row_max);
+      if (lane == 0) red[parity][1][warp] = row_max;
+      __syncthreads();
+      row_max = warp_max(lane < nw ? red[parity][1][lane] : 0.f);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int v = i * nt + tid;
+      float y[8];
+      normed(rv[i], wv[i], rstd, a.w_off, y);
+      float amax = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(y[e]));
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1)
+        if (o < lpg) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      if (lpg == 0) amax = row_max;
+      if (v >= nvec) continue;                 // no shuffle below
+      const bool first = lpg == 0 ? v == 0 : (v & (lpg - 1)) == 0;
+      const int64_t g = lpg == 0 ? 0 : v / lpg;
+      uint2 q;
+      if (DT == kMxFp8) {
+        const int se = mx_exponent(amax);
+        const float inv = __uint_as_float((uint32_t)(127 - se) << 23);   // 2^-se, exact
+        q.x = e4m3x4(y, inv);
+        q.y = e4m3x4(y + 4, inv);
+        if (first) a.sf[mx_sf_index(m, g, a.K)] = (uint8_t)(se + 127);
+      } else {
+        const float sc = group_scale<DT>(amax);
+        if (sc >= 0x1p-100f) {
+          const float inv = __fdiv_rn(1.0f, sc);
+          q.x = DT == kInt8 ? int8x4(y, inv) : e4m3x4(y, inv);
+          q.y = DT == kInt8 ? int8x4(y + 4, inv) : e4m3x4(y + 4, inv);
+        } else {                               // the reciprocal may not be a number
+          q.x = pack4_codes<DT == kMxFp8 ? kFp8 : DT>(y, sc);
+          q.y = pack4_codes<DT == kMxFp8 ? kFp8 : DT>(y + 4, sc);
+        }
+        if (first) a.s[g * a.M + m] = sc;
+      }
+      *reinterpret_cast<uint2*>(a.q + m * a.ldq + 8 * (int64_t)v) = q;
+      if (a.h)
+        reinterpret_cast<uint4*>(a.h + m * a.ldh)[v] =
+            make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]),
+                       pack_bf16(y[6], y[7]));
+    }
+  }
+}
+
+// Lanes of a group for the vector kernel, 0 for the whole row, -1 if it does not fit.
+int group_lanes(const NormArgs& a) {
+  if (a.group >= a.K) return 0;
+  const int64_t l = a.group / 8;
+  return a.group % 8 == 0 && l <= 32 && (l & (l - 1)) == 0 ? (int)l : -1;
+}
+
+bool vec_ok(const NormArgs& a) {
+  auto al = [](const void* p, int64_t ld, int n, int bytes) {
+    return p == nullptr || ((reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0 && ld % n == 0);
+  };
+  return a.K % 8 == 0 && a.K <= 32768 && group_lanes(a) >= 0 && al(a.x, a.ldx, 8, 16) &&
+         al(a.res, a.ldr, 8, 16) && al(a.w, 0, 8, 16) && al(a.res_out, a.ldro, 8, 16) &&
+         al(a.h, a.ldh, 8, 16) && al(a.q, a.ldq, 8, 8);
+}
+
+template <int DT, int V>
+cudaError_t launch_vec(const NormArgs& a, cudaStream_t st) {
+  const int64_t nvec = a.K / 8;
+  const int nt = (int)((nvec + 32 * V - 1) / (32 * V)) * 32;
+  const int64_t fit = std::max(1, 2048 / nt);            // CTAs of an SM, by its threads
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(a.M, 148 * fit));
+  cfg.blockDim = dim3((unsigned)nt);
+  cfg.stream = st;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, norm_vec_kernel<DT, V>, a, group_lanes(a));
+}
+
 template <int DT>
 cudaError_t launch_any(const NormArgs& a, cudaStream_t st) {
   const size_t smem = (size_t)a.K * 2;
@@ -117,7 +302,11 @@ cudaError_t launch_any(const NormArgs& a, cudaStream_t st) {
 
 template <int DT>
 cudaError_t launch_dt(const NormArgs& a, cudaStream_t st) {
-  return launch_any<DT>(a, st);
+  if (!vec_ok(a)) return launch_any<DT>(a, st);
+  // few rows: a vector a thread, for latency; many: more loads in flight a thread
+  if (a.M <= 148 && a.K <= 8192) return launch_vec<DT, 1>(a, st);
+  if (a.K <= 2048) return launch_vec<DT, 1>(a, st);
+  return a.K <= 16384 ? launch_vec<DT, 4>(a, st) : launch_vec<DT, 8>(a, st);
 }
 
 }  // namespace

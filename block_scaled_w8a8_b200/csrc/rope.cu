@@ -10,6 +10,7 @@
 // (in fp32 the product alone would be off by 0.06 rad); the remaining
 // fraction, below half a turn, goes to fp32 sine and cosine.
 #include <algorithm>
+#include <cstdint>
 
 #include "bq_common.cuh"
 #include "layer_ops.h"
@@ -26,6 +27,21 @@ __device__ __forceinline__ void turn_of(int32_t pos, double turns, float mscale,
   sincospif(2.0f * f, &sn, &cs);
   sn *= mscale;
   cs *= mscale;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// A pair turned; the same roundings wherever it is done, so that the kernels
+// agree to the bit.
+__device__ __forceinline__ float turned_a(float a, float b, float c, float s) {
+  return fmaf(a, c, -__fmul_rn(b, s));
+}
+__device__ __forceinline__ float turned_b(float a, float b, float c, float s) {
+  return fmaf(b, c, __fmul_rn(a, s));
 }
 
 // Any rot, strides and alignment: a thread per pair or copied element.
@@ -48,25 +64,111 @@ __global__ void __launch_bounds__(256) rope_any_kernel(const RopeArgs a) {
     const float va = bf16_bits_to_float(x[ia]), vb = bf16_bits_to_float(x[ib]);
     float sn, cs;
     turn_of(a.pos[t], a.turns[e], a.mscale, sn, cs);
-    o[ia] = float_to_bf16_bits(va * cs - vb * sn);
-    o[ib] = float_to_bf16_bits(vb * cs + va * sn);
+    o[ia] = float_to_bf16_bits(turned_a(va, vb, cs, sn));
+    o[ib] = float_to_bf16_bits(turned_b(va, vb, cs, sn));
   }
+}
+
+// Rows of whole 16-byte vectors: a CTA has TT tokens; its threads form the
+// rot / 2 sines and cosines of each token once (the fp64 product is all that a
+// pair costs beyond fp32), then turn 16 bytes of each half (or four neighbouring
+// pairs) of all heads.  Memory-bound: every byte is read and written once.
+constexpr int kVecThreads = 256;
+
+template <bool INTER>
+__global__ void __launch_bounds__(kVecThreads) rope_vec_kernel(const RopeArgs a, const int TT) {
+  extern __shared__ float2 cs[];               // [TT][rot / 2] {cos, sin}
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int half = (int)(a.rot / 2), H = (int)a.H, tid = threadIdx.x;
+  const int64_t t0 = (int64_t)blockIdx.x * TT;
+  const int nt = (int)min((int64_t)TT, a.T - t0);
+  for (int e = tid; e < nt * half; e += kVecThreads) {
+    const int t = e / half;
+    float sn, c;
+    turn_of(a.pos[t0 + t], a.turns[e - t * half], a.mscale, sn, c);
+    cs[e] = make_float2(c, sn);
+  }
+  __syncthreads();
+  // vectors of a head: those with pairs, then those that are copied
+  const int np = INTER ? (int)a.rot / 8 : half / 8;
+  const int nc = a.out == a.x ? 0 : (int)(a.D - a.rot) / 8, per = np + nc;
+  const int total = nt * H * per;
+  for (int i = tid; i < total; i += kVecThreads) {
+    const int th = i / per, e = i - th * per, t = th / H, h = th - t * H;
+    const uint16_t* x = a.x + (t0 + t) * a.ldt + h * a.ldh;
+    uint16_t* o = a.out + (t0 + t) * a.ldot + h * a.ldoh;
+    if (e >= np) {
+      const int64_t d = a.rot + 8 * (e - np);
+      *reinterpret_cast<uint4*>(o + d) = *reinterpret_cast<const uint4*>(x + d);
+      continue;
+    }
+    const float4* f = reinterpret_cast<const float4*>(cs + t * half + (INTER ? 4 : 8) * e);
+    if (INTER) {
+      uint4 v = *reinterpret_cast<const uint4*>(x + 8 * e);
+      uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float4 q = f[k >> 1];
+        const float c = k & 1 ? q.z : q.x, s = k & 1 ? q.w : q.y;
+        const float p = __uint_as_float(w[k] << 16), r = __uint_as_float(w[k] & 0xFFFF0000u);
+        w[k] = pack_bf16(turned_a(p, r, c, s), turned_b(p, r, c, s));
+      }
+      *reinterpret_cast<uint4*>(o + 8 * e) = v;
+    } else {
+      uint4 va = *reinterpret_cast<const uint4*>(x + 8 * e);
+      uint4 vb = *reinterpret_cast<const uint4*>(x + half + 8 * e);
+      uint32_t *wa = reinterpret_cast<uint32_t*>(&va), *wb = reinterpret_cast<uint32_t*>(&vb);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float4 q = f[k];
+        const float a0 = __uint_as_float(wa[k] << 16), a1 = __uint_as_float(wa[k] & 0xFFFF0000u);
+        const float b0 = __uint_as_float(wb[k] << 16), b1 = __uint_as_float(wb[k] & 0xFFFF0000u);
+        wa[k] = pack_bf16(turned_a(a0, b0, q.x, q.y), turned_a(a1, b1, q.z, q.w));
+        wb[k] = pack_bf16(turned_b(a0, b0, q.x, q.y), turned_b(a1, b1, q.z, q.w));
+      }
+      *reinterpret_cast<uint4*>(o + 8 * e) = va;
+      *reinterpret_cast<uint4*>(o + half + 8 * e) = vb;
+    }
+  }
+}
+
+bool vec_ok(const RopeArgs& a) {
+  auto al = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
+  const int64_t unit = a.interleaved ? 8 : 16;           // of rot
+  return al(a.x) && al(a.out) && a.ldt % 8 == 0 && a.ldh % 8 == 0 && a.ldot % 8 == 0 &&
+         a.ldoh % 8 == 0 && a.D % 8 == 0 && a.rot % unit == 0 && a.rot <= 1024 &&
+         a.H * a.D <= (1 << 22);
 }
 
 }  // namespace
 
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st) {
   if (a.T == 0 || a.H == 0) return cudaSuccess;
-  const int64_t work = a.T * a.H * (a.D - a.rot / 2);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)std::min<int64_t>((work + 255) / 256, 148 * 16));
-  cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
+  if (vec_ok(a)) {
+    // many tokens: as many a CTA as one round of its threads has angles for
+    const int64_t half = std::max<int64_t>(1, a.rot / 2);
+    int64_t tt = a.T > 148 * 8 ? std::max<int64_t>(1, kVecThreads / half) : 1;
+    tt = std::min<int64_t>(tt, 8);
+    const int64_t grid = (a.T + tt - 1) / tt;
+    if (grid <= INT32_MAX) {
+      cfg.gridDim = dim3((unsigned)grid);
+      cfg.blockDim = dim3(kVecThreads);
+      cfg.dynamicSmemBytes = (size_t)(tt * half) * sizeof(float2);
+      return a.interleaved ? cudaLaunchKernelEx(&cfg, rope_vec_kernel<true>, a, (int)tt)
+                           : cudaLaunchKernelEx(&cfg, rope_vec_kernel<false>, a, (int)tt);
+    }
+  }
+  const int64_t work = a.T * a.H * (a.D - a.rot / 2);
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>((work + 255) / 256, 148 * 16));
+  cfg.blockDim = dim3(256);
   return cudaLaunchKernelEx(&cfg, rope_any_kernel, a);
 }
 
