@@ -15,7 +15,7 @@ Layouts (see include/bq.h):
 from __future__ import annotations
 
 import ctypes
-import math
+import functools
 import os
 import threading
 from typing import NamedTuple
@@ -539,75 +539,102 @@ def moe_combine(y, inv_perm, topk_w, out=None):
 
 
 # ---- between two linears: norm, rotary positions, cache, attention ----------
+# These calls are short kernels in a decoding step, so their checks are kept
+# cheap: device indices, no message formatted unless it is raised.
 
-def _need(cond: bool, msg: str):
-    if not cond:
-        raise ValueError(msg)
+def _bad(msg: str):
+    raise ValueError(msg)
+
+
+def _index(t, name: str) -> int:
+    """The index of t's CUDA device (raises for anything else)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    i = t.get_device()
+    if i < 0:
+        raise ValueError(f"{name} must be on a CUDA device (libbq has no CPU path)")
+    return i
+
+
+def _there(t, name: str, dev: int):
+    if _index(t, name) != dev:
+        _bad(f"{name} must be on cuda:{dev}, not {t.device}")
 
 
 class _on:
-    """The device of a call's tensors as the current one, for the launch."""
+    """Device `idx` as the current one, for the launch."""
+    __slots__ = ("idx", "prev")
 
-    def __init__(self, dev: torch.device):
-        self.idx = dev.index
+    def __init__(self, idx: int):
+        self.idx = idx
 
     def __enter__(self):
-        self.prev = torch.cuda.current_device()
+        self.prev = torch._C._cuda_getDevice()
         if self.prev != self.idx:
             torch.cuda.set_device(self.idx)
+        return torch._C._cuda_getCurrentRawStream(self.idx)
 
     def __exit__(self, *exc):
         if self.prev != self.idx:
             torch.cuda.set_device(self.prev)
 
 
-def _same_device(dev, **tensors):
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        _cuda(t, name)
-        _need(t.device == dev, f"{name} must be on {dev}, not {t.device}")
+def _rows(t, name: str, dtype, M: int, K: int, dev: int) -> int:
+    """Row stride of a [M, K] tensor of `dtype` with unit column stride."""
+    _there(t, name, dev)
+    if t.dtype is not dtype or t.dim() != 2 or t.shape != (M, K):
+        _bad(f"{name} must be {dtype} [{M}, {K}], not {t.dtype} {list(t.shape)}")
+    ld, unit = t.stride()
+    if unit != 1 and K > 1:
+        _bad(f"{name} must have unit column stride")
+    if M <= 1:
+        return K
+    if ld < K:
+        _bad(f"{name}: rows overlap")
+    return ld
 
 
-def _matrix(t, name, dtype, M, K):
-    _need(t.dtype == dtype and t.dim() == 2 and t.shape[0] == M and t.shape[1] == K,
-          f"{name} must be {dtype} [{M}, {K}]")
-    _need(t.stride(1) == 1 or K <= 1, f"{name} must have unit column stride")
-    _need(t.stride(0) >= K or M <= 1, f"{name}: rows overlap")
+def _dense(t, name: str, dtype, shape: tuple, dev: int) -> int:
+    """Address of a dense tensor of that shape."""
+    _there(t, name, dev)
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _bad(f"{name} must be {dtype} {list(shape)}, dense, not {t.dtype} {list(t.shape)}")
+    return t.data_ptr()
 
 
-def _row_stride(t, K):
-    return max(t.stride(0), K)
-
-
-def _rmsnorm(x, weight, eps, residual, weight_offset, want_h, q, scales, res_out, h, call):
-    _cuda(x, "x")
-    _need(x.dim() == 2, "x must be bfloat16 [M, K]")
+def _rmsnorm(fn, x, weight, eps, residual, weight_offset, want_h, group, q, scales, res_out, h):
+    dev = _index(x, "x")
+    if x.dim() != 2:
+        _bad("x must be bfloat16 [M, K]")
     M, K = x.shape
-    dev, bf16 = x.device, torch.bfloat16
+    bf16, device = torch.bfloat16, x.device
+    ldx = _rows(x, "x", bf16, M, K, dev)
+    ldq = ldr = ldro = ldh = K
+    pr = pro = ph = None
     if q is None:
-        q = torch.empty(M, K, dtype=torch.uint8, device=dev)
-    if residual is not None and res_out is None:
-        res_out = torch.empty(M, K, dtype=bf16, device=dev)
-    if want_h and h is None:
-        h = torch.empty(M, K, dtype=bf16, device=dev)
-    _same_device(dev, weight=weight, residual=residual, q=q, scales=scales, res_out=res_out, h=h)
-    _need(weight.dtype == bf16 and weight.shape == (K,) and weight.is_contiguous(),
-          f"weight must be bfloat16 [{K}], dense")
-    _matrix(x, "x", bf16, M, K)
-    _matrix(q, "q", torch.uint8, M, K)
-    for t, name in ((residual, "residual"), (res_out, "res_out"), (h, "h")):
-        if t is not None:
-            _matrix(t, name, bf16, M, K)
-    with _on(dev):
-        _check(call(
-            x.data_ptr(), _row_stride(x, K), _opt(residual, "residual"),
-            K if residual is None else _row_stride(residual, K), weight.data_ptr(),
-            weight_offset, eps, M, K, q.data_ptr(), _row_stride(q, K), scales.data_ptr(),
-            _opt(res_out, "res_out"), K if res_out is None else _row_stride(res_out, K),
-            _opt(h, "h"), K if h is None else _row_stride(h, K), _stream(dev)))
-    return (q, scales) + ((res_out,) if res_out is not None else ()) + \
-        ((h,) if h is not None else ())
+        q = torch.empty(M, K, dtype=torch.uint8, device=device)
+    else:
+        ldq = _rows(q, "q", torch.uint8, M, K, dev)
+    if residual is not None:
+        ldr, pr = _rows(residual, "residual", bf16, M, K, dev), residual.data_ptr()
+        if res_out is None:
+            res_out = torch.empty(M, K, dtype=bf16, device=device)
+            pro = res_out.data_ptr()
+    if res_out is not None and pro is None:
+        ldro, pro = _rows(res_out, "res_out", bf16, M, K, dev), res_out.data_ptr()
+    if h is not None:
+        ldh, ph = _rows(h, "h", bf16, M, K, dev), h.data_ptr()
+    elif want_h:
+        h = torch.empty(M, K, dtype=bf16, device=device)
+        ph = h.data_ptr()
+    pw = _dense(weight, "weight", bf16, (K,), dev)
+    with _on(dev) as stream:
+        _check(fn(x.data_ptr(), ldx, pr, ldr, pw, weight_offset, eps, M, K, *group, q.data_ptr(),
+                  ldq, scales.data_ptr(), pro, ldro, ph, ldh, stream))
+    out = (q, scales)
+    if res_out is not None:
+        out += (res_out,)
+    return out if h is None else out + (h,)
 
 
 def rmsnorm_quant(x, weight, eps=1e-6, residual=None, group_k=128, dtype=INT8, weight_offset=0.0,
@@ -617,39 +644,43 @@ def rmsnorm_quant(x, weight, eps=1e-6, residual=None, group_k=128, dtype=INT8, w
     x, residual: bf16 [M, K]; weight: bf16 [K].  Returns (q [M, K], s [Kb, M]),
     then res_out = bf16(x + residual) if there is a residual (or res_out is
     given), then h = bf16(y) if want_h.  res_out may be residual or x."""
+    dev = _index(x, "x")
+    if x.dim() != 2:
+        _bad("x must be bfloat16 [M, K]")
+    if group_k < 1:
+        _bad("group_k must be >= 1")
     M, K = x.shape
-    _need(group_k >= 1, "group_k must be >= 1")
     if s is None:
-        s = torch.empty(cdiv(K, group_k), M, dtype=torch.float32, device=x.device)
-    _need(s.dtype == torch.float32 and s.shape == (cdiv(K, group_k), M) and s.is_contiguous(),
-          f"s must be float32 [{cdiv(K, group_k)}, {M}], dense")
-
-    def call(x_, ldx, r_, ldr, w_, off, eps_, M_, K_, q_, ldq, s_, ro, ldro, h_, ldh, st):
-        return lib().bq_rmsnorm_quant(x_, ldx, r_, ldr, w_, off, eps_, M_, K_, group_k, dtype, q_,
-                                      ldq, s_, ro, ldro, h_, ldh, st)
-
-    return _rmsnorm(x, weight, eps, residual, weight_offset, want_h, q, s, res_out, h, call)
+        s = torch.empty(-(-K // group_k), M, dtype=torch.float32, device=x.device)
+    else:
+        _dense(s, "s", torch.float32, (-(-K // group_k), M), dev)
+    return _rmsnorm(lib().bq_rmsnorm_quant, x, weight, eps, residual, weight_offset, want_h,
+                    (group_k, dtype), q, s, res_out, h)
 
 
 def mx_rmsnorm_quant(x, weight, eps=1e-6, residual=None, weight_offset=0.0, want_h=False, q=None,
                      sf=None, res_out=None, h=None):
     """rmsnorm_quant with MXFP8 codes and scale atoms, for mx_gemm."""
+    dev = _index(x, "x")
+    if x.dim() != 2:
+        _bad("x must be bfloat16 [M, K]")
     M, K = x.shape
-    n = mx_scale_bytes(M, K)
     if sf is None:
-        sf = torch.empty(n, dtype=torch.uint8, device=x.device)
-    _need(sf.dtype == torch.uint8 and sf.numel() >= n and sf.is_contiguous(),
-          f"sf must be uint8, dense, of at least {n} bytes")
-    return _rmsnorm(x, weight, eps, residual, weight_offset, want_h, q, sf, res_out, h,
-                    lib().bq_mx_rmsnorm_quant)
+        sf = torch.empty(mx_scale_bytes(M, K), dtype=torch.uint8, device=x.device)
+    else:
+        _there(sf, "sf", dev)
+        if sf.dtype is not torch.uint8 or not sf.is_contiguous() or \
+                sf.numel() < cdiv(M, 128) * (K // 128) * 512:
+            _bad(f"sf must be uint8, dense, of at least {mx_scale_bytes(M, K)} bytes")
+    return _rmsnorm(lib().bq_mx_rmsnorm_quant, x, weight, eps, residual, weight_offset, want_h,
+                    (), q, sf, res_out, h)
 
 
 def rope_frequencies(rot_dim, base=10000.0, scaling=ROPE_PLAIN, factor=1.0, orig_max_pos=0,
                      beta_fast=32.0, beta_slow=1.0, device="cuda"):
     """(turns, mscale) for rope(): float64 [rot_dim/2] turns per position on
     `device`, and the factor on the rotated pairs (1 but for ROPE_YARN)."""
-    _need(rot_dim >= 0, "rot_dim must be >= 0")
-    host = torch.empty(rot_dim // 2, dtype=torch.float64)
+    host = torch.empty(max(rot_dim, 0) // 2, dtype=torch.float64)
     ms = _F32(0.0)
     _check(lib().bq_rope_frequencies(
         rot_dim, base, scaling, factor, orig_max_pos, beta_fast, beta_slow,
@@ -657,35 +688,39 @@ def rope_frequencies(rot_dim, base=10000.0, scaling=ROPE_PLAIN, factor=1.0, orig
     return host.to(device), ms.value
 
 
-def _heads(t, name, T, H, D):
+def _heads(t, name: str, T: int, H: int, D: int, dev: int):
     """Token and head strides of a bf16 [T, H, D] tensor with unit last stride."""
-    _need(t.dtype == torch.bfloat16 and t.dim() == 3 and t.shape[0] == T and t.shape[1] == H and
-          t.shape[2] == D, f"{name} must be bfloat16 [{T}, {H}, {D}]")
-    st = t.stride()
-    _need(st[2] == 1 or D <= 1, f"{name} must have unit stride in its last dimension")
-    return st[0], st[1]
+    _there(t, name, dev)
+    if t.dtype is not torch.bfloat16 or t.shape != (T, H, D):
+        _bad(f"{name} must be bfloat16 [{T}, {H}, {D}], not {t.dtype} {list(t.shape)}")
+    st, sh, unit = t.stride()
+    if unit != 1 and D > 1:
+        _bad(f"{name} must have unit stride in its last dimension")
+    return st, sh
 
 
 def rope(x, positions, freqs, layout=ROPE_HALF, mscale=1.0, out=None):
     """Rotary positions on bf16 x [T, H, D] (any token and head strides): the
     first 2 * len(freqs) dimensions of each head are turned, the rest copied.
     positions: int32 [T]; freqs, mscale: from rope_frequencies.  out may be x."""
-    _cuda(x, "x")
-    _need(x.dim() == 3, "x must be bfloat16 [T, H, D]")
+    dev = _index(x, "x")
+    if x.dim() != 3:
+        _bad("x must be bfloat16 [T, H, D]")
     T, H, D = x.shape
+    xt, xh = _heads(x, "x", T, H, D, dev)
     if out is None:
         out = torch.empty(T, H, D, dtype=torch.bfloat16, device=x.device)
-    _same_device(x.device, positions=positions, freqs=freqs, out=out)
-    _need(positions.dtype == torch.int32 and positions.shape == (T,) and
-          (positions.stride(0) == 1 or T <= 1), f"positions must be int32 [{T}], dense")
-    _need(freqs.dtype == torch.float64 and freqs.dim() == 1 and freqs.is_contiguous(),
-          "freqs must be float64 [rot_dim / 2], dense")
-    xt, xh = _heads(x, "x", T, H, D)
-    ot, oh = _heads(out, "out", T, H, D)
-    with _on(x.device):
-        _check(lib().bq_rope(x.data_ptr(), xt, xh, positions.data_ptr(), freqs.data_ptr(), T, H,
-                             D, 2 * freqs.shape[0], layout, mscale, out.data_ptr(), ot, oh,
-                             _stream(x.device)))
+        ot, oh = H * D, D
+    else:
+        ot, oh = _heads(out, "out", T, H, D, dev)
+    pp = _dense(positions, "positions", torch.int32, (T,), dev)
+    if freqs.dim() != 1:
+        _bad("freqs must be float64 [rot_dim / 2]")
+    half = freqs.shape[0]
+    pf = _dense(freqs, "freqs", torch.float64, (half,), dev)
+    with _on(dev) as stream:
+        _check(lib().bq_rope(x.data_ptr(), xt, xh, pp, pf, T, H, D, 2 * half, layout, mscale,
+                             out.data_ptr(), ot, oh, stream))
     return out
 
 
@@ -701,7 +736,8 @@ class KvCache(NamedTuple):
 
 def kv_cache(n_pages, n_heads, page_size, head_dim, block_t=16, dtype=INT8, device="cuda"):
     """An empty cache."""
-    _need(block_t >= 1 and page_size % block_t == 0, "block_t must divide page_size")
+    if block_t < 1 or page_size % block_t:
+        _bad("block_t must divide page_size")
     codes = [torch.zeros(n_pages, n_heads, page_size, head_dim, dtype=torch.uint8, device=device)
              for _ in range(2)]
     scales = [torch.zeros(n_pages, n_heads, page_size // block_t, dtype=torch.float32,
@@ -709,35 +745,33 @@ def kv_cache(n_pages, n_heads, page_size, head_dim, block_t=16, dtype=INT8, devi
     return KvCache(*codes, *scales, dtype)
 
 
-def _cache_args(cache: KvCache, dev):
-    k, v, ks, vs, dtype = cache
-    _same_device(dev, k=k, v=v, ks=ks, vs=vs)
-    _need(k.dtype == torch.uint8 and v.dtype == torch.uint8 and k.dim() == 4 and
-          v.shape == k.shape and k.is_contiguous() and v.is_contiguous(),
-          "cache codes must be uint8 [n_pages, Hkv, page_size, D], dense and alike")
-    P, H, page, D = k.shape
-    _need(ks.dtype == torch.float32 and vs.dtype == torch.float32 and ks.dim() == 3 and
-          vs.shape == ks.shape and ks.shape[0] == P and ks.shape[1] == H and
-          ks.is_contiguous() and vs.is_contiguous(),
-          "cache scales must be float32 [n_pages, Hkv, page_size / block_t], dense and alike")
-    nb = ks.shape[2]
-    _need(page >= 1 and nb >= 1 and page % nb == 0, "block_t must divide page_size")
-    return P, H, page, D, page // nb
+def _cache_args(k, v, ks, vs, dev: int):
+    """(n_pages, Hkv, page_size, D, block_t) and the four addresses."""
+    if k.dim() != 4 or ks.dim() != 3:
+        _bad("cache codes must be uint8 [n_pages, Hkv, page_size, D], scales float32 "
+             "[n_pages, Hkv, page_size / block_t]")
+    shape = k.shape
+    n_pages, H, page, D = shape
+    blocks = ks.shape[2]
+    sshape = (n_pages, H, blocks)
+    ptrs = (_dense(k, "cache.k", torch.uint8, shape, dev),
+            _dense(v, "cache.v", torch.uint8, shape, dev),
+            _dense(ks, "cache.ks", torch.float32, sshape, dev),
+            _dense(vs, "cache.vs", torch.float32, sshape, dev))
+    if page < 1 or blocks < 1 or page % blocks:
+        _bad("block_t must divide page_size")
+    return n_pages, H, page, D, page // blocks, ptrs
 
 
-def _batch_args(seq_offsets, kv_lens, page_table, dev):
-    _same_device(dev, seq_offsets=seq_offsets, kv_lens=kv_lens, page_table=page_table)
-    B = kv_lens.shape[0] if kv_lens.dim() == 1 else -1
-    _need(B >= 0 and kv_lens.dtype == torch.int32 and kv_lens.is_contiguous(),
-          "kv_lens must be int32 [B], dense")
-    _need(seq_offsets.dtype == torch.int32 and seq_offsets.shape == (B + 1,) and
-          seq_offsets.is_contiguous(), f"seq_offsets must be int32 [{B + 1}], dense")
-    _need(page_table.dtype == torch.int32 and page_table.dim() == 2 and
-          page_table.shape[0] == B, f"page_table must be int32 [{B}, pages]")
-    cols = page_table.shape[1]
-    _need(page_table.stride(1) == 1 or cols <= 1, "page_table must have unit column stride")
-    _need(page_table.stride(0) >= 0, "page_table: negative stride")
-    return B, max(page_table.stride(0), cols) if B > 1 else cols, cols
+def _batch_args(seq_offsets, kv_lens, page_table, dev: int):
+    """(offsets, lengths, table, ld_table, table_cols, B)."""
+    if kv_lens.dim() != 1 or page_table.dim() != 2:
+        _bad("kv_lens must be int32 [B], page_table int32 [B, pages]")
+    B = kv_lens.shape[0]
+    lens = _dense(kv_lens, "kv_lens", torch.int32, (B,), dev)
+    off = _dense(seq_offsets, "seq_offsets", torch.int32, (B + 1,), dev)
+    ld = _rows(page_table, "page_table", torch.int32, B, page_table.shape[1], dev)
+    return off, lens, page_table.data_ptr(), ld, page_table.shape[1], B
 
 
 def kv_append(cache: KvCache, k, v, seq_offsets, kv_lens, page_table):
@@ -745,22 +779,19 @@ def kv_append(cache: KvCache, k, v, seq_offsets, kv_lens, page_table):
     head strides), into the cache.  Rows seq_offsets[b] .. seq_offsets[b+1] are
     the last tokens of sequence b, whose length with them is kv_lens[b];
     page_table int32 [B, pages].  Lengths and pages are read on the device."""
-    _cuda(k, "k")
-    dev = k.device
-    P, H, page, D, bt = _cache_args(cache, dev)
-    B, ld, cols = _batch_args(seq_offsets, kv_lens, page_table, dev)
-    _same_device(dev, v=v)
-    T = k.shape[0]
-    kt, kh = _heads(k, "k", T, H, D)
-    vt, vh = _heads(v, "v", T, H, D)
-    with _on(dev):
-        _check(lib().bq_kv_append(
-            k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, seq_offsets.data_ptr(),
-            kv_lens.data_ptr(), page_table.data_ptr(), ld, cols, B, T, H, D, P, page, bt,
-            cache.dtype, cache.k.data_ptr(), cache.v.data_ptr(), cache.ks.data_ptr(),
-            cache.vs.data_ptr(), _stream(dev)))
+    dev = _index(k, "k")
+    ck, cv, cks, cvs, dtype = cache
+    P, H, page, D, bt, ptrs = _cache_args(ck, cv, cks, cvs, dev)
+    batch = _batch_args(seq_offsets, kv_lens, page_table, dev)
+    T = k.shape[0] if k.dim() else -1
+    kt, kh = _heads(k, "k", T, H, D, dev)
+    vt, vh = _heads(v, "v", T, H, D, dev)
+    with _on(dev) as stream:
+        _check(lib().bq_kv_append(k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, *batch, T, H, D, P,
+                                  page, bt, dtype, *ptrs, stream))
 
 
+@functools.lru_cache(maxsize=1024)
 def kv_attention_workspace_size(B, T, Hq, Hkv, D, max_q_len, max_kv_len, page_size,
                                 block_t) -> int:
     n = ctypes.c_size_t(0)
@@ -777,32 +808,35 @@ def kv_attention(q, cache: KvCache, seq_offsets, kv_lens, page_table, max_q_len,
     a causal row sees, 0 for all.  lse: float32 [T, Hq] to fill, or None.
     Rows at and behind seq_offsets[B] are left as they are.  Without ws, the
     workspace is allocated for the call."""
-    _cuda(q, "q")
-    dev = q.device
-    P, H, page, D, bt = _cache_args(cache, dev)
-    B, ld, cols = _batch_args(seq_offsets, kv_lens, page_table, dev)
-    _need(q.dim() == 3, "q must be bfloat16 [T, Hq, D]")
+    dev = _index(q, "q")
+    ck, cv, cks, cvs, dtype = cache
+    P, H, page, D, bt, ptrs = _cache_args(ck, cv, cks, cvs, dev)
+    batch = _batch_args(seq_offsets, kv_lens, page_table, dev)
+    if q.dim() != 3:
+        _bad("q must be bfloat16 [T, Hq, D]")
     T, Hq = q.shape[0], q.shape[1]
-    qt, qh = _heads(q, "q", T, Hq, D)
+    qt, qh = _heads(q, "q", T, Hq, D, dev)
     if out is None:
-        out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=dev)
-    ot, oh = _heads(out, "out", T, Hq, D)
-    _same_device(dev, out=out, lse=lse, ws=ws)
-    if lse is not None:
-        _need(lse.dtype == torch.float32 and lse.shape == (T, Hq) and lse.is_contiguous(),
-              f"lse must be float32 [{T}, {Hq}], dense")
+        out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=q.device)
+        ot, oh = Hq * D, D
+    else:
+        ot, oh = _heads(out, "out", T, Hq, D, dev)
+    pl = None if lse is None else _dense(lse, "lse", torch.float32, (T, Hq), dev)
+    need = kv_attention_workspace_size(batch[5], T, Hq, H, D, max_q_len, max_kv_len, page, bt)
+    pws = wsb = 0
+    if ws is not None:
+        _there(ws, "ws", dev)
+        if not ws.is_contiguous():
+            _bad("ws must be dense")
+    elif need:
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+    if ws is not None:
+        pws, wsb = ws.data_ptr(), ws.numel() * ws.element_size()
     if scale is None:
-        scale = 1.0 / math.sqrt(D)
-    with _on(dev):
-        if ws is None:
-            n = kv_attention_workspace_size(B, T, Hq, H, D, max_q_len, max_kv_len, page, bt)
-            if n:
-                ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        scale = D ** -0.5
+    with _on(dev) as stream:
         _check(lib().bq_kv_attention(
-            q.data_ptr(), qt, qh, seq_offsets.data_ptr(), kv_lens.data_ptr(),
-            page_table.data_ptr(), ld, cols, B, T, Hq, H, D, max_q_len, max_kv_len,
-            cache.k.data_ptr(), cache.v.data_ptr(), cache.ks.data_ptr(), cache.vs.data_ptr(), P,
-            page, bt, cache.dtype, scale, int(causal), window, out.data_ptr(), ot, oh,
-            None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(),
-            0 if ws is None else ws.numel() * ws.element_size(), _stream(dev)))
+            q.data_ptr(), qt, qh, *batch, T, Hq, H, D, max_q_len, max_kv_len, *ptrs, P, page, bt,
+            dtype, scale, 1 if causal else 0, window, out.data_ptr(), ot, oh, pl, pws, wsb,
+            stream))
     return out
