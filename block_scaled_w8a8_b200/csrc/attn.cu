@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(kAnyWarps * 32) attn_any_kernel(const AttnArgs
   const int64_t t = item / a.Hq;
   const int h = (int)(item - t * a.Hq);
   if (t >= a.b.T) return;
-  const int b = kv::last_at_most(a.b.B, t, [&](int i) { return (int64_t)a.b.off[i]; });
+  const int b = kv::seq_of(a.b, t);
   kv::Seq s;
   if (!kv::load_seq(a.b, a.c.page, b, s) || s.n > a.max_q || s.len > a.max_kv) {
     if (lane == 0) record_status(a.status, kStatusBadInput, 0x701u);
@@ -96,46 +96,63 @@ __global__ void __launch_bounds__(kAnyWarps * 32) attn_any_kernel(const AttnArgs
   if (a.lse && lane == 0) a.lse[t * a.Hq + h] = l == 0.f ? -INFINITY : m + logf(l);
 }
 
-// Joins the splits of a row in split order: a warp per (row, query head).
-constexpr int kMergeWarps = 4;
-
-__global__ void __launch_bounds__(kMergeWarps * 32)
+// Joins the splits of a row: NW warps per (row, query head) take the splits in
+// turn, and their sums are joined in warp order.  NW = 1 up to 4 splits, 8 above:
+// the splits' rows are loaded side by side instead of one latency each.
+template <int NW>
+__global__ void __launch_bounds__(128 * (NW > 4 ? 2 : 1))
 attn_merge_kernel(const AttnArgs a, const AttnParts p) {
+  __shared__ float so[NW][kMaxD];
+  __shared__ float sl[NW];
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int lane = threadIdx.x & 31;
-  const int64_t item = (int64_t)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int w = NW > 1 ? warp : 0;
+  const int64_t item = NW > 1 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + warp;
   const int64_t t = item / a.Hq;
-  const int h = (int)(item - t * a.Hq);
+  const int h = (int)(item - t * a.Hq), D = a.c.D;
   if (t >= a.b.T) return;
-  const int b = kv::last_at_most(a.b.B, t, [&](int i) { return (int64_t)a.b.off[i]; });
+  const int b = kv::seq_of(a.b, t);
   kv::Seq s;
   if (!kv::load_seq(a.b, a.c.page, b, s) || s.n > a.max_q || s.len > a.max_kv || t < s.row0 ||
       t >= s.row0 + s.n)
     return;                          // recorded by the kernel before, or nobody's row
-  const float4* stat = reinterpret_cast<const float4*>(p.stat) + item * p.splits;
-  float m = -INFINITY, mo = -INFINITY, l = 0.f;
-  for (int i = lane; i < p.splits; i += 32) {
-    const float4 x = stat[i];
-    m = fmaxf(m, x.x);
-    mo = fmaxf(mo, x.z);
-  }
-  m = warp_max(m);
+  const float2* stat = reinterpret_cast<const float2*>(p.stat) + item * p.splits;
+  float mo = -INFINITY;
+  for (int i = lane; i < p.splits; i += 32) mo = fmaxf(mo, stat[i].y);
   mo = warp_max(mo);
-  float acc[kMaxD / 32] = {};
-  for (int i = 0; i < p.splits; ++i) {
-    const float4 x = stat[i];
-    if (x.y == 0.f) continue;
-    l += x.y * attn::ex2(x.x - attn::finite(m));
-    const float f = attn::ex2(x.z - attn::finite(mo));
-    const float* o = p.o + (item * p.splits + i) * a.c.D;
+  float l = 0.f, acc[kMaxD / 32] = {};
+#pragma unroll 4
+  for (int i = w; i < p.splits; i += NW) {
+    const float2 x = stat[i];
+    if (x.x == 0.f) continue;
+    const float f = attn::ex2(x.y - attn::finite(mo));
+    l += x.x * f;
+    const float* o = p.o + (item * p.splits + i) * D;
 #pragma unroll
     for (int e = 0; e < kMaxD / 32; ++e)
-      if (lane + 32 * e < a.c.D) acc[e] = fmaf(o[lane + 32 * e], f, acc[e]);
+      if (lane + 32 * e < D) acc[e] = fmaf(o[lane + 32 * e], f, acc[e]);
   }
+  if constexpr (NW == 1) {
 #pragma unroll
-  for (int e = 0; e < kMaxD / 32; ++e)
-    if (lane + 32 * e < a.c.D) attn::write_row(a, t, h, lane + 32 * e, m, l, mo, acc[e]);
+    for (int e = 0; e < kMaxD / 32; ++e)
+      if (lane + 32 * e < D) attn::write_row(a, t, h, lane + 32 * e, l, mo, acc[e]);
+  } else {
+    if (lane == 0) sl[w] = l;
+#pragma unroll
+    for (int e = 0; e < kMaxD / 32; ++e)
+      if (lane + 32 * e < D) so[w][lane + 32 * e] = acc[e];
+    __syncthreads();
+    for (int d = threadIdx.x; d < D; d += 32 * NW) {
+      float sum = 0.f, v = 0.f;
+#pragma unroll
+      for (int i = 0; i < NW; ++i) {
+        sum += sl[i];
+        v += so[i][d];
+      }
+      attn::write_row(a, t, h, d, sum, mo, v);
+    }
+  }
 }
 
 template <class... Args>
@@ -183,8 +200,8 @@ size_t attn_workspace_bytes(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64
 
 cudaError_t launch_attn_merge(const AttnArgs& a, const AttnParts& p, cudaStream_t st) {
   const int64_t items = a.b.T * a.Hq;
-  return launch_pdl(attn_merge_kernel, (items + kMergeWarps - 1) / kMergeWarps, kMergeWarps * 32,
-                    st, a, p);
+  return p.splits <= 4 ? launch_pdl(attn_merge_kernel<1>, (items + 3) / 4, 128, st, a, p)
+                       : launch_pdl(attn_merge_kernel<8>, items, 256, st, a, p);
 }
 
 cudaError_t launch_kv_attention(const AttnArgs& a, void* ws, cudaStream_t st) {
@@ -197,7 +214,7 @@ cudaError_t launch_kv_attention(const AttnArgs& a, void* ws, cudaStream_t st) {
     p.splits = plan_splits(path, a.b.B, a.Hq, a.c.H, a.max_q, a.max_kv);
     if (p.splits > 1) {
       p.stat = static_cast<float*>(ws);
-      p.o = p.stat + 4 * items * p.splits;
+      p.o = p.stat + (2 * items * p.splits + 3) / 4 * 4;
     }
     cudaError_t e =
         path == Path::kTc ? launch_attn_tc(a, p, st) : launch_attn_decode(a, p, st);

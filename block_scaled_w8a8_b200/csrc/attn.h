@@ -6,18 +6,18 @@
 
 namespace bq {
 
-// Partial results of a row (token t, query head h), one per split: fp32 O[D] of
-// the weights 2^(z + lg2 vs - mo), and {m, l, mo}: the running maximum of the
-// scores z (in log2 units), l = sum 2^(z - m), and O's own reference mo.  A
+// Partial results of a row (token t, query head h), one per split: fp32 O[D] in
+// units of 2^mo, and {l, mo}: mo is the split's reference for the row's y = z +
+// lg2 vs (z the scores in log2 units, vs the value scales), l = sum 2^(z - mo).  A
 // split that saw no key of the row has l = 0 and writes no O.
 struct AttnParts {
   float* o;        // [T * Hq][splits][D]
-  float* stat;     // [T * Hq][splits][4]
+  float* stat;     // [T * Hq][splits][2]
   int splits;      // 1: no partials, the kernel writes the result itself
 };
 
 inline size_t attn_part_bytes(int64_t rows, int splits, int64_t D) {
-  return splits <= 1 ? 0 : (size_t)rows * (size_t)splits * (size_t)(D + 4) * sizeof(float);
+  return splits <= 1 ? 0 : (size_t)rows * (size_t)splits * (size_t)(D + 2) * sizeof(float) + 16;
 }
 
 cudaError_t launch_attn_merge(const AttnArgs& a, const AttnParts& p, cudaStream_t st);

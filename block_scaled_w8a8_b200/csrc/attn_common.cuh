@@ -55,6 +55,15 @@ __device__ __forceinline__ float lg2(float x) {
   return y;
 }
 
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Value scales below this count as it (their values are below 2^-93).
+constexpr float kMinVs = 0x1p-100f;
+
 // A running maximum as the reference of a difference: 0 while nothing was seen.
 __device__ __forceinline__ float finite(float m) { return m == -INFINITY ? 0.f : m; }
 
@@ -63,6 +72,17 @@ __device__ __forceinline__ uint4 ld_codes16(const uint8_t* p) {
   asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
+}
+
+// The D / 8 code bytes of one token that a lane of the value product holds.
+template <int D>
+__device__ __forceinline__ void ld_codes(const uint8_t* p, uint32_t (&w)[D / 32]) {
+  if constexpr (D == 64)
+    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
+                 : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+  else
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
 }
 
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
@@ -118,16 +138,15 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return y;
 }
 
-// out[tok, head, d] and, from the thread of d = 0, lse: from the maximum m and
-// sum l of the scores (log2 units) and acc = O in units of 2^mo.
-__device__ __forceinline__ void write_row(const AttnArgs& a, int64_t tok, int head, int d, float m,
-                                          float l, float mo, float acc) {
-  // l == 0: the row saw no key; mo == -inf: only values with a scale of 0
-  const bool none = l == 0.f || mo == -INFINITY;
-  const float v = none ? 0.f : acc * __fdiv_rn(ex2(mo - finite(m)), l);
-  a.out[tok * a.ldo + (int64_t)head * a.ho + d] = float_to_bf16_bits(v);
+// out[tok, head, d] and, from the thread of d = 0, lse: from l = sum 2^(z - mo)
+// and acc = O in units of 2^mo.
+__device__ __forceinline__ void write_row(const AttnArgs& a, int64_t tok, int head, int d, float l,
+                                          float mo, float acc) {
+  // l == 0: the row saw no key; a NaN stays one
+  a.out[tok * a.ldo + (int64_t)head * a.ho + d] =
+      float_to_bf16_bits(l == 0.f ? 0.f : __fdiv_rn(acc, l));
   if (a.lse && d == 0)
-    a.lse[tok * a.Hq + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    a.lse[tok * a.Hq + head] = l == 0.f ? -INFINITY : (mo + log2f(l)) * 0.6931471805599453f;
 }
 
 }  // namespace attn

@@ -13,16 +13,20 @@
 //                 dims from r D / 8 on, of tokens 2c, 2c+1, 2c+8, 2c+9 (8 lanes =
 //                 one row of D bytes); a byte permute pairs two tokens' codes.
 //                 P^T is S^T's accumulator, transposed in registers (movmatrix).
-// The next group's codes are requested before this group's are used.
+// A group's registers take the next group's codes as soon as the product that
+// reads them has been issued, so a warp has about 4 KB under way and needs no
+// second set of registers.
 //
 // Precision.  Codes are exact in fp16 (INT8: 1152 is subtracted from the
 // fp16 number 1024 + 128 + q; e4m3: the hardware conversion).  A query row is
 // scaled by a power of two to a largest magnitude of 2^14 .. 2^15 and is then
 // exact in fp16 too (8 significant bits), but for elements below 2^-29 of the
-// row's largest.  Scores, running maxima and sums are fp32.  The weights are
-// rounded to fp16 (half a step: 2^-11): they include the value's block scale,
-// 2^(z + lg2 vs - mo) with mo the running maximum of that exponent, so the
-// largest is 1 whatever the scales are; l = sum 2^(z - m) has its own maximum.
+// row's largest.  Scores and sums are fp32.  The weights are rounded to fp16
+// (half a step: 2^-11); as in attn_tc.cu they include the value's block scale,
+// 2^(y - mo) with y = z + lg2 vs, and l += weight / vs.  mo is the row's largest y
+// of the first keys a warp sees; later weights are formed with it as it stands,
+// and only where one passes 2^10 (fp16 ends at 2^16) is mo raised and O rescaled,
+// so that a group of keys costs no search for a maximum across lanes.
 // Masked weights are set to zero, and the codes of values outside the rows'
 // range are replaced by zero before the product, so no stale byte enters a sum.
 #include <algorithm>
@@ -40,44 +44,34 @@ using namespace attn;
 
 constexpr int kWarps = 4;
 
-template <int D>
-struct VWords {                 // code bytes of one token that a lane holds: D / 8
-  uint32_t w[D / 32];
-};
-
-template <int D>
-__device__ __forceinline__ VWords<D> load_v(const uint8_t* p) {
-  VWords<D> v;
-  if constexpr (D == 64) {
-    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
-                 : "=r"(v.w[0]), "=r"(v.w[1]) : "l"(p));
-  } else {
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3]) : "l"(p));
-  }
-  return v;
-}
-
 // One group of 16 tokens as it comes from memory.
-template <int D>
+template <int D, bool UNI>
 struct Group {
   uint4 k[2][D / 64];           // tokens r, r + 8
-  VWords<D> v[4];               // tokens 2c, 2c + 1, 2c + 8, 2c + 9
-  float ks[2], vs[2];           // scales of tokens r, r + 8
-  bool ok;                      // the group's page exists (warp-uniform)
+  uint32_t v[4][D / 32];        // tokens 2c, 2c + 1, 2c + 8, 2c + 9: D / 8 bytes each
+  float ks[UNI ? 1 : 2], vs[UNI ? 1 : 2];   // scales of tokens r, r + 8 (UNI: of all)
 };
 
-template <int DT, int D, int NR>
+// Where a group of 16 tokens lies: its page of the sequence and its first slot
+// there, moved on by a fixed number of tokens without a division.
+struct Place {
+  int idx, slot;
+};
+
+// UNI: block_t is a multiple of 16, so that the group shares its scales.
+template <int DT, int D, int NR, bool UNI>
 __global__ void __launch_bounds__(kWarps * 32)
 attn_decode_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles) {
   constexpr int NG = 128 / D;              // groups of 16 tokens in flight: 4 KB of codes a warp
   constexpr int KS = D / 16;               // k-steps of the score product
   constexpr int R = 8 * NR;
+  constexpr int SC = UNI ? 1 : 2;
   __shared__ float so[kWarps][R][D + 4];
-  __shared__ float st[kWarps][R][3];
+  __shared__ float st[kWarps][R][2];
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
+  const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   const int split = (int)(blockIdx.x % (unsigned)parts.splits);
   const int bt_ = (int)(blockIdx.x / (unsigned)parts.splits);
   const int rt = bt_ % row_tiles, b = bt_ / row_tiles, hk = blockIdx.y;
@@ -94,6 +88,66 @@ attn_decode_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles)
   const Range all = tile_range(a, s, i_lo, i_hi);
   const Range part = split_range(all, split, parts.splits, 16 * NG);
 
+  const int page = a.c.page, bt = a.c.bt, nblk = page / bt;
+  const unsigned bt_inv = bt > 1 ? (unsigned)(0x100000000ull / (unsigned)bt + 1) : 0u;
+  constexpr int STEP = 16 * NG, STRIDE = kWarps * STEP;
+  const int stride_idx = STRIDE / page, stride_slot = STRIDE % page;
+  const int32_t* table = a.b.table + (int64_t)b * a.b.ld_table;
+  const uint8_t* kbase = a.c.k + r * D + 16 * c;
+  const uint8_t* vbase = a.c.v + 2 * c * D + r * (D / 8);
+  int t = part.lo + warp * STEP;
+  Place at[NG];                            // of the groups whose page is to be fetched next
+  int32_t pg[NG];                          // page of the groups to be loaded next
+#pragma unroll
+  for (int u = 0; u < NG; ++u) {
+    const int tu = t + 16 * u;
+    at[u].idx = tu / page;
+    at[u].slot = tu - at[u].idx * page;
+    pg[u] = tu < part.hi ? table[at[u].idx] : -1;
+  }
+  // page and slot of a group -> first code row and scale, or -1
+  auto row_of = [&](int u) -> int64_t {
+    return pg[u] >= 0 && (int64_t)pg[u] < a.c.n_pages ? (int64_t)pg[u] * a.c.H + hk : -1;
+  };
+  Group<D, UNI> G[NG];
+  bool ok[NG];                             // the group's page exists (warp-uniform)
+  auto load_k = [&](int u, int64_t ph) {
+    const int slot = at[u].slot;
+    if (ph < 0) return;
+    const uint8_t* p = kbase + (ph * page + slot) * D;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) G[u].k[h][i] = ld_codes16(p + h * 8 * D + 64 * i);
+#pragma unroll
+    for (int h = 0; h < SC; ++h) {
+      const unsigned x = (unsigned)(slot + (UNI ? 0 : r + 8 * h));
+      G[u].ks[h] = a.c.ks[ph * nblk + (bt > 1 ? __umulhi(x, bt_inv) : x)];
+    }
+  };
+  auto load_v = [&](int u, int64_t ph) {
+    const int slot = at[u].slot;
+    if (ph < 0) return;
+    const uint8_t* p = vbase + (ph * page + slot) * D;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) ld_codes<D>(p + ((e & 1) + 8 * (e >> 1)) * D, G[u].v[e]);
+#pragma unroll
+    for (int h = 0; h < SC; ++h) {
+      const unsigned x = (unsigned)(slot + (UNI ? 0 : r + 8 * h));
+      G[u].vs[h] = a.c.vs[ph * nblk + (bt > 1 ? __umulhi(x, bt_inv) : x)];
+    }
+  };
+  int64_t ph[NG];
+#pragma unroll
+  for (int u = 0; u < NG; ++u) {
+    ph[u] = row_of(u);
+    ok[u] = ph[u] >= 0;
+    load_k(u, ph[u]);
+    load_v(u, ph[u]);
+    if (!ok[u] && t + 16 * u < part.hi && lane == 0)
+      record_status(a.status, kStatusBadInput, 0x712u);
+  }
+
   // queries: row R0 + 8 nt + r of lane (r, c), dims 64 i + 16 c .. + 15
   uint32_t qf[NR][KS][2];
   float rowfac[NR][2];
@@ -101,185 +155,191 @@ attn_decode_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles)
 #pragma unroll
   for (int nt = 0; nt < NR; ++nt) {
     const int row = R0 + 8 * nt + r;
-    float v[KS][4], amax = 0.f;
     const bool on = row < n_rows;
     const uint16_t* q = a.q + (int64_t)(s.row0 + (on ? row / g : 0)) * a.ldq +
                         (int64_t)(hk * g + (on ? row % g : 0)) * a.hq;
+    uint32_t w[KS][2];                     // bf16 pairs: word 2 (k-step) + e of the row's part
+    const bool vec = (reinterpret_cast<uintptr_t>(q) & 15) == 0;
+#pragma unroll
+    for (int ks = 0; ks < KS; ks += 2) {
+      const uint16_t* p = q + 64 * (ks >> 2) + 16 * c + 4 * (ks & 3);
+      uint4 x = make_uint4(0u, 0u, 0u, 0u);
+      if (on && vec) x = *reinterpret_cast<const uint4*>(p);
+      else if (on)
+        x = make_uint4(p[0] | (uint32_t)p[1] << 16, p[2] | (uint32_t)p[3] << 16,
+                       p[4] | (uint32_t)p[5] << 16, p[6] | (uint32_t)p[7] << 16);
+      w[ks][0] = x.x; w[ks][1] = x.y; w[ks + 1][0] = x.z; w[ks + 1][1] = x.w;
+    }
+    float amax = 0.f;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[ks][e] = on ? bf16_bits_to_float(q[64 * (ks >> 2) + 16 * c + 4 * (ks & 3) + e]) : 0.f;
-        amax = fmaxf(amax, fabsf(v[ks][e]));
-      }
+      for (int e = 0; e < 2; ++e)
+        amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[ks][e] << 16)),
+                                 fabsf(__uint_as_float(w[ks][e] & 0xFFFF0000u))));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
     float up, down;
     row_power(amax, up, down);
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      qf[nt][ks][0] = pack_f16(v[ks][0] * up, v[ks][1] * up);
-      qf[nt][ks][1] = pack_f16(v[ks][2] * up, v[ks][3] * up);
-    }
+    for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        qf[nt][ks][e] = pack_f16(__uint_as_float(w[ks][e] << 16) * up,
+                                 __uint_as_float(w[ks][e] & 0xFFFF0000u) * up);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       rowfac[nt][j] = __shfl_sync(0xffffffffu, down, 4 * (2 * c + j)) * (a.scale * kLog2e);
+      // rows behind the last stand in for it (their queries are zero, nothing is written)
       const int i = min((R0 + 8 * nt + 2 * c + j) / g, s.n - 1);
       row_range(a, s, i, row_lo[nt][j], row_hi[nt][j]);
     }
   }
   // every row of the tile sees the tokens of [in_lo, in_hi)
-  int dummy, in_lo, in_hi;
-  row_range(a, s, i_hi, in_lo, dummy);
-  row_range(a, s, i_lo, dummy, in_hi);
+  int unused, in_lo, in_hi;
+  row_range(a, s, i_hi, in_lo, unused);
+  row_range(a, s, i_lo, unused, in_hi);
 
-  float o[NR][KS][4], m[NR][2], l[NR][2], mo[NR][2];
+  float o[NR][KS][4], l[NR][2], mo[NR][2];
 #pragma unroll
   for (int nt = 0; nt < NR; ++nt) {
 #pragma unroll
     for (int i = 0; i < KS; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
-    m[nt][0] = m[nt][1] = mo[nt][0] = mo[nt][1] = -INFINITY;
+    mo[nt][0] = mo[nt][1] = -INFINITY;
     l[nt][0] = l[nt][1] = 0.f;
   }
 
-  const int page = a.c.page, bt = a.c.bt, nblk = page / bt;
-  const unsigned bt_inv = bt > 1 ? (unsigned)(0x100000000ull / (unsigned)bt + 1) : 0u;
-  auto page_at = [&](int t) -> int64_t {
-    return t < part.hi ? kv::page_of(a.b, a.c, b, t) : -1;
-  };
-  auto load = [&](Group<D>& G, int t0, int64_t pg) {
-    G.ok = pg >= 0;
-    if (!G.ok) {
-      if (t0 < part.hi && lane == 0) record_status(a.status, kStatusBadInput, 0x712u);
-      return;
-    }
-    const int64_t ph = pg * a.c.H + hk;
-    const int in_page = t0 % page;
-    const uint8_t* kp = a.c.k + (ph * page + in_page + r) * D + 16 * c;
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < D / 64; ++i) G.k[h][i] = ld_codes16(kp + h * 8 * D + 64 * i);
-    const uint8_t* vp = a.c.v + (ph * page + in_page + 2 * c) * D + r * (D / 8);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) G.v[e] = load_v<D>(vp + ((e & 1) + 8 * (e >> 1)) * D);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const unsigned x = (unsigned)(in_page + r + 8 * h);
-      const int64_t blk = ph * nblk + (bt > 1 ? __umulhi(x, bt_inv) : x);
-      G.ks[h] = a.c.ks[blk];
-      G.vs[h] = a.c.vs[blk];
-    }
-  };
-
-  constexpr int STEP = 16 * NG;
-  int t = part.lo + warp * STEP;
-  Group<D> cur[NG];
-  int64_t pg[NG];
-#pragma unroll
-  for (int u = 0; u < NG; ++u) load(cur[u], t + 16 * u, page_at(t + 16 * u));
-#pragma unroll
-  for (int u = 0; u < NG; ++u) pg[u] = page_at(t + kWarps * STEP + 16 * u);
-  for (; t < part.hi; t += kWarps * STEP) {
-    Group<D> nxt[NG];
+  for (; t < part.hi; t += STRIDE) {
+    // the next groups' pages
 #pragma unroll
     for (int u = 0; u < NG; ++u) {
-      const int tn = t + kWarps * STEP + 16 * u;
-      load(nxt[u], tn, pg[u]);
-      pg[u] = page_at(tn + kWarps * STEP);
+      at[u].idx += stride_idx;
+      at[u].slot += stride_slot;
+      if (at[u].slot >= page) {
+        at[u].slot -= page;
+        ++at[u].idx;
+      }
+      pg[u] = t + STRIDE + 16 * u < part.hi ? table[at[u].idx] : -1;
     }
-    const bool whole = t >= in_lo && t + STEP <= in_hi;
-    // scores
-    float z[NR][NG][4];
+    bool whole = t >= in_lo && t + STEP <= in_hi;
+#pragma unroll
+    for (int u = 0; u < NG; ++u) whole = whole && ok[u];
+    // scores, then y: e = 0, 1 rows 2c, 2c + 1 of token r; e = 2, 3 of token r + 8
+    float y[NR][NG][4];
 #pragma unroll
     for (int u = 0; u < NG; ++u) {
 #pragma unroll
       for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) z[nt][u][e] = 0.f;
+        for (int e = 0; e < 4; ++e) y[nt][u][e] = 0.f;
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
         uint32_t f[4];
-        codes_to_f16<DT>(word_of(cur[u].k[0][ks >> 2], ks & 3), f[0], f[2]);
-        codes_to_f16<DT>(word_of(cur[u].k[1][ks >> 2], ks & 3), f[1], f[3]);
+        codes_to_f16<DT>(word_of(G[u].k[0][ks >> 2], ks & 3), f[0], f[2]);
+        codes_to_f16<DT>(word_of(G[u].k[1][ks >> 2], ks & 3), f[1], f[3]);
 #pragma unroll
-        for (int nt = 0; nt < NR; ++nt) mma_f16(z[nt][u], f, qf[nt][ks]);
+        for (int nt = 0; nt < NR; ++nt) mma_f16(y[nt][u], f, qf[nt][ks]);
       }
     }
-    // weights: e = 0, 1 rows 2c, 2c + 1 of token r; e = 2, 3 of token r + 8
-    uint32_t pf[NR][NG][2];
+    float iv[NG][SC];
 #pragma unroll
-    for (int nt = 0; nt < NR; ++nt) {
-      float zo[NG][4], mx[2] = {-INFINITY, -INFINITY}, mxo[2] = {-INFINITY, -INFINITY};
+    for (int u = 0; u < NG; ++u) {
+      float lv[SC];
+#pragma unroll
+      for (int h = 0; h < SC; ++h) {
+        const float vs = ok[u] ? fmaxf(G[u].vs[h], kMinVs) : 1.f;
+        lv[h] = lg2(vs);
+        iv[u][h] = rcp(vs);
+      }
+#pragma unroll
+      for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          y[nt][u][e] = fmaf(y[nt][u][e], G[u].ks[UNI ? 0 : e >> 1] * rowfac[nt][e & 1],
+                             lv[UNI ? 0 : e >> 1]);
+    }
+    // keys of the group after next are under way from here on
+    int64_t ph_next[NG];
+#pragma unroll
+    for (int u = 0; u < NG; ++u) {
+      ph_next[u] = row_of(u);
+      if (ph_next[u] < 0 && t + STRIDE + 16 * u < part.hi && lane == 0)
+        record_status(a.status, kStatusBadInput, 0x712u);
+      load_k(u, ph_next[u]);
+    }
+    if (!whole) {
 #pragma unroll
       for (int u = 0; u < NG; ++u)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float ks = cur[u].ks[h], lv = lg2(cur[u].vs[h]);
-          const int tok = t + 16 * u + r + 8 * h;
+        for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            float x = z[nt][u][2 * h + j] * (ks * rowfac[nt][j]), y = x + lv;
-            if (!whole || !cur[u].ok) {
-              const bool on = cur[u].ok && tok >= row_lo[nt][j] && tok < row_hi[nt][j];
-              x = on ? x : -INFINITY;
-              y = on ? y : -INFINITY;
-            }
-            z[nt][u][2 * h + j] = x;
-            zo[u][2 * h + j] = y;
-            mx[j] = fmaxf(mx[j], x);
-            mxo[j] = fmaxf(mxo[j], y);
+          for (int e = 0; e < 4; ++e) {
+            const int tok = t + 16 * u + r + 8 * (e >> 1), j = e & 1;
+            if (!ok[u] || tok < row_lo[nt][j] || tok >= row_hi[nt][j]) y[nt][u][e] = -INFINITY;
           }
-        }
-      float keep[2];
+    }
+    // weights
+    uint32_t pf[NR][NG][2];
+#pragma unroll
+    for (int nt = 0; nt < NR; ++nt) {
+      bool far = false;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
+        float mx = y[nt][0][j];
 #pragma unroll
-        for (int sh = 4; sh <= 16; sh <<= 1) {
-          mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], sh));
-          mxo[j] = fmaxf(mxo[j], __shfl_xor_sync(0xffffffffu, mxo[j], sh));
+        for (int u = 0; u < NG; ++u)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) mx = fmaxf(mx, y[nt][u][2 * h + j]);
+        // the first keys of a row, or one far above its reference
+        far = far || mx > mo[nt][j] + 10.f;
+      }
+      if (__any_sync(0xffffffffu, far)) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float mx = mo[nt][j];
+#pragma unroll
+          for (int u = 0; u < NG; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) mx = fmaxf(mx, y[nt][u][2 * h + j]);
+#pragma unroll
+          for (int sh = 4; sh <= 16; sh <<= 1)
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
+          const float keep = ex2(mo[nt][j] - finite(mx));
+          l[nt][j] *= keep;
+          mo[nt][j] = mx;
+#pragma unroll
+          for (int i = 0; i < KS; ++i) {
+            o[nt][i][j] *= keep;
+            o[nt][i][2 + j] *= keep;
+          }
         }
-        mx[j] = fmaxf(mx[j], m[nt][j]);
-        mxo[j] = fmaxf(mxo[j], mo[nt][j]);
-        l[nt][j] *= ex2(m[nt][j] - finite(mx[j]));
-        keep[j] = ex2(mo[nt][j] - finite(mxo[j]));
-        m[nt][j] = mx[j];
-        mo[nt][j] = mxo[j];
-        mx[j] = finite(mx[j]);
-        mxo[j] = finite(mxo[j]);
       }
-      if (__any_sync(0xffffffffu, keep[0] != 1.f || keep[1] != 1.f)) {
-#pragma unroll
-        for (int i = 0; i < KS; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[nt][i][e] *= keep[e & 1];
-      }
+      const float ref[2] = {finite(mo[nt][0]), finite(mo[nt][1])};
 #pragma unroll
       for (int u = 0; u < NG; ++u) {
+        float p[4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float p[2];
+        for (int e = 0; e < 4; ++e) p[e] = ex2(y[nt][u][e] - ref[e & 1]);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            l[nt][j] += ex2(z[nt][u][2 * h + j] - mx[j]);
-            p[j] = ex2(zo[u][2 * h + j] - mxo[j]);
-          }
-          pf[nt][u][h] = transpose8(pack_f16(p[0], p[1]));
-        }
+        for (int j = 0; j < 2; ++j)
+          l[nt][j] = UNI ? fmaf(p[j] + p[2 + j], iv[u][0], l[nt][j])
+                         : fmaf(p[j], iv[u][0], fmaf(p[2 + j], iv[u][SC - 1], l[nt][j]));
+        pf[nt][u][0] = transpose8(pack_f16(p[0], p[1]));
+        pf[nt][u][1] = transpose8(pack_f16(p[2], p[3]));
       }
     }
     // values
 #pragma unroll
     for (int u = 0; u < NG; ++u) {
-      if (t + 16 * u < part.lo || t + 16 * u + 16 > part.hi || !cur[u].ok || t + 16 * u < all.lo) {
+      if (!ok[u] || t + 16 * u < all.lo || t + 16 * u + 16 > part.hi) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int tok = t + 16 * u + 2 * c + (e & 1) + 8 * (e >> 1);
-          const bool on = cur[u].ok && tok >= all.lo && tok < part.hi;
+          const bool on = ok[u] && tok >= all.lo && tok < part.hi;
 #pragma unroll
-          for (int w = 0; w < D / 32; ++w) cur[u].v[e].w[w] = on ? cur[u].v[e].w[w] : 0u;
+          for (int w = 0; w < D / 32; ++w) G[u].v[e][w] = on ? G[u].v[e][w] : 0u;
         }
       }
 #pragma unroll
@@ -287,9 +347,9 @@ attn_decode_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles)
         uint32_t f0[4], f1[4];           // m-tiles 2w, 2w + 1
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint32_t x = cur[u].v[2 * h].w[w], y = cur[u].v[2 * h + 1].w[w];
-          codes_to_f16<DT>(__byte_perm(x, y, 0x5140), f0[2 * h], f0[2 * h + 1]);
-          codes_to_f16<DT>(__byte_perm(x, y, 0x7362), f1[2 * h], f1[2 * h + 1]);
+          const uint32_t x = G[u].v[2 * h][w], z = G[u].v[2 * h + 1][w];
+          codes_to_f16<DT>(__byte_perm(x, z, 0x5140), f0[2 * h], f0[2 * h + 1]);
+          codes_to_f16<DT>(__byte_perm(x, z, 0x7362), f1[2 * h], f1[2 * h + 1]);
         }
 #pragma unroll
         for (int nt = 0; nt < NR; ++nt) {
@@ -297,9 +357,9 @@ attn_decode_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles)
           mma_f16(o[nt][2 * w + 1], f1, pf[nt][u]);
         }
       }
+      load_v(u, ph_next[u]);
+      ok[u] = ph_next[u] >= 0;
     }
-#pragma unroll
-    for (int u = 0; u < NG; ++u) cur[u] = nxt[u];
   }
 
   // the four warps' parts, joined in warp order
@@ -312,9 +372,8 @@ attn_decode_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles)
       for (int sh = 4; sh <= 16; sh <<= 1) x += __shfl_xor_sync(0xffffffffu, x, sh);
       const int row = 8 * nt + 2 * c + j;
       if (r == 0) {
-        st[warp][row][0] = m[nt][j];
-        st[warp][row][1] = x;
-        st[warp][row][2] = mo[nt][j];
+        st[warp][row][0] = x;
+        st[warp][row][1] = mo[nt][j];
       }
 #pragma unroll
       for (int i = 0; i < KS; ++i) {
@@ -327,32 +386,29 @@ attn_decode_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles)
   for (int e = threadIdx.x; e < R * D; e += kWarps * 32) {
     const int row = e / D, d = e % D;
     if (R0 + row >= n_rows) break;
-    float M = -INFINITY, MO = -INFINITY;
+    float MO = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      M = fmaxf(M, st[w][row][0]);
-      MO = fmaxf(MO, st[w][row][2]);
-    }
+    for (int w = 0; w < kWarps; ++w) MO = fmaxf(MO, st[w][row][1]);
     float sum = 0.f, acc = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      sum += st[w][row][1] * ex2(st[w][row][0] - finite(M));
-      acc += so[w][row][d] * ex2(st[w][row][2] - finite(MO));
+      const float f = ex2(st[w][row][1] - finite(MO));
+      sum += st[w][row][0] * f;
+      acc += so[w][row][d] * f;
     }
     const int64_t tok = s.row0 + (R0 + row) / g;
     const int head = hk * g + (R0 + row) % g;
     if (parts.splits == 1) {
-      write_row(a, tok, head, d, M, sum, MO, acc);
+      write_row(a, tok, head, d, sum, MO, acc);
     } else {
       const int64_t p = (tok * a.Hq + head) * parts.splits + split;
       if (sum != 0.f) parts.o[p * D + d] = acc;
-      if (d == 0)
-        *reinterpret_cast<float4*>(parts.stat + 4 * p) = make_float4(M, sum, MO, 0.f);
+      if (d == 0) *reinterpret_cast<float2*>(parts.stat + 2 * p) = make_float2(sum, MO);
     }
   }
 }
 
-template <int DT, int D, int NR>
+template <int DT, int D, int NR, bool UNI>
 cudaError_t launch_t(const AttnArgs& a, const AttnParts& p, cudaStream_t st) {
   const int64_t rows = (int64_t)a.max_q * (a.Hq / a.c.H);
   const int64_t tiles = (rows + 8 * NR - 1) / (8 * NR);
@@ -367,15 +423,20 @@ cudaError_t launch_t(const AttnArgs& a, const AttnParts& p, cudaStream_t st) {
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_decode_kernel<DT, D, NR>, a, p, (int)tiles);
+  return cudaLaunchKernelEx(&cfg, attn_decode_kernel<DT, D, NR, UNI>, a, p, (int)tiles);
+}
+
+template <int DT, int D>
+cudaError_t launch_d(const AttnArgs& a, const AttnParts& p, cudaStream_t st) {
+  const bool few = (int64_t)a.max_q * (a.Hq / a.c.H) <= 8;
+  if (a.c.bt % 16 == 0)
+    return few ? launch_t<DT, D, 1, true>(a, p, st) : launch_t<DT, D, 2, true>(a, p, st);
+  return few ? launch_t<DT, D, 1, false>(a, p, st) : launch_t<DT, D, 2, false>(a, p, st);
 }
 
 template <int DT>
 cudaError_t launch_dt(const AttnArgs& a, const AttnParts& p, cudaStream_t st) {
-  const bool few = (int64_t)a.max_q * (a.Hq / a.c.H) <= 8;
-  if (a.c.D == 64)
-    return few ? launch_t<DT, 64, 1>(a, p, st) : launch_t<DT, 64, 2>(a, p, st);
-  return few ? launch_t<DT, 128, 1>(a, p, st) : launch_t<DT, 128, 2>(a, p, st);
+  return a.c.D == 64 ? launch_d<DT, 64>(a, p, st) : launch_d<DT, 128>(a, p, st);
 }
 
 }  // namespace

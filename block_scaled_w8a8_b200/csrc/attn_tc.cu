@@ -58,7 +58,6 @@ constexpr int kSoftRegs = 152, kConvRegs = 104;
 constexpr int kSplitRegs = 256 * kSoftRegs + 256 * kConvRegs;
 static_assert(kSplitRegs <= 65536, "register file");
 constexpr float kLazy = 8.0f;           // how far y may pass its reference (log2)
-constexpr float kMinVs = 0x1p-100f;
 
 template <int D>
 struct Lay {
@@ -676,7 +675,7 @@ attn_tc_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles) {
       }
       if (row_on) {
         if (!whole)
-          *reinterpret_cast<float4*>(parts.stat + 4 * pi) = make_float4(mo, l, mo, 0.f);
+          *reinterpret_cast<float2*>(parts.stat + 2 * pi) = make_float2(l, mo);
         else if (a.lse)
           a.lse[tok * a.Hq + head] =
               l == 0.f ? -INFINITY : (mo + log2f(l)) * 0.6931471805599453f;

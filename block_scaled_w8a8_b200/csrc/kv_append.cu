@@ -33,17 +33,10 @@ struct Unit {
   int64_t page;
 };
 
-// Called by whole warps: the lanes count the sequences that begin at or before u
-// side by side (one or two memory latencies instead of log2 B).
+// Called by whole warps.
 __device__ __forceinline__ bool find_unit(const AppendArgs& a, int64_t u, Unit& w) {
   const int bt = a.c.bt, lane = threadIdx.x & 31;
-  if (a.b.B <= 1024) {
-    int n = 0;
-    for (int i = lane; i < a.b.B; i += 32) n += kv::first_unit(a.b, bt, i) <= u ? 1 : 0;
-    w.b = max(0, __reduce_add_sync(0xffffffffu, n) - 1);
-  } else {
-    w.b = kv::last_at_most(a.b.B, u, [&](int i) { return kv::first_unit(a.b, bt, i); });
-  }
+  w.b = kv::last_at_most(a.b.B, u, [&](int i) { return kv::first_unit(a.b, bt, i); });
   kv::Seq s;
   if (!kv::load_seq(a.b, a.c.page, w.b, s) || s.len < s.n) {
     if (lane == 0) record_status(a.status, kStatusBadInput, 0x601u);

@@ -10,14 +10,26 @@ namespace bq {
 namespace kv {
 
 // Largest b in [0, B) with key(b) <= x, for a nondecreasing key(); 0 if none.
+// Called by whole warps: the lanes count side by side, one or two memory
+// latencies instead of log2 B.
 template <class F>
 __device__ __forceinline__ int last_at_most(int B, int64_t x, F key) {
+  if (B <= 1024) {
+    int n = 0;
+    for (int i = threadIdx.x & 31; i < B; i += 32) n += key(i) <= x ? 1 : 0;
+    return max(0, __reduce_add_sync(0xffffffffu, n) - 1);
+  }
   int lo = 0, hi = B;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (key(mid) <= x) lo = mid; else hi = mid;
   }
   return lo;
+}
+
+// The sequence whose rows row t may belong to.
+__device__ __forceinline__ int seq_of(const KvBatch& kb, int64_t t) {
+  return last_at_most(kb.B, t, [&](int i) { return (int64_t)kb.off[i]; });
 }
 
 // Rows and length of sequence b; false if they cannot be used (then nothing
