@@ -556,85 +556,75 @@ def _index(t, name: str) -> int:
     return i
 
 
-def _there(t, name: str, dev: int):
+def _wrong(t, name: str, dtype, shape, dev: int):
+    """Raises for what the checks below found wrong with t."""
     if _index(t, name) != dev:
         _bad(f"{name} must be on cuda:{dev}, not {t.device}")
-
-
-class _on:
-    """Device `idx` as the current one, for the launch."""
-    __slots__ = ("idx", "prev")
-
-    def __init__(self, idx: int):
-        self.idx = idx
-
-    def __enter__(self):
-        self.prev = torch._C._cuda_getDevice()
-        if self.prev != self.idx:
-            torch.cuda.set_device(self.idx)
-        return torch._C._cuda_getCurrentRawStream(self.idx)
-
-    def __exit__(self, *exc):
-        if self.prev != self.idx:
-            torch.cuda.set_device(self.prev)
+    _bad(f"{name} must be {dtype} {list(shape)}, with dense rows that do not overlap, not "
+         f"{t.dtype} {list(t.shape)} with strides {t.stride()}")
 
 
 def _rows(t, name: str, dtype, M: int, K: int, dev: int) -> int:
     """Row stride of a [M, K] tensor of `dtype` with unit column stride."""
-    _there(t, name, dev)
-    if t.dtype is not dtype or t.dim() != 2 or t.shape != (M, K):
-        _bad(f"{name} must be {dtype} [{M}, {K}], not {t.dtype} {list(t.shape)}")
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != (M, K):
+        _wrong(t, name, dtype, (M, K), dev)
     ld, unit = t.stride()
-    if unit != 1 and K > 1:
-        _bad(f"{name} must have unit column stride")
-    if M <= 1:
-        return K
-    if ld < K:
-        _bad(f"{name}: rows overlap")
-    return ld
+    if (unit != 1 and K > 1) or (ld < K and M > 1):
+        _wrong(t, name, dtype, (M, K), dev)
+    return ld if ld > K else K
 
 
 def _dense(t, name: str, dtype, shape: tuple, dev: int) -> int:
     """Address of a dense tensor of that shape."""
-    _there(t, name, dev)
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        _bad(f"{name} must be {dtype} {list(shape)}, dense, not {t.dtype} {list(t.shape)}")
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape or \
+            not t.is_contiguous():
+        _wrong(t, name, dtype, shape, dev)
     return t.data_ptr()
 
 
+_cuda_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
+def _launch(fn, dev: int, *args):
+    """fn(*args, stream) with `dev` as the current device; its current stream."""
+    if _cuda_device() == dev:
+        status = fn(*args, _raw_stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, _raw_stream(dev))
+    if status:
+        _check(status)
+
+
 def _rmsnorm(fn, x, weight, eps, residual, weight_offset, want_h, group, q, scales, res_out, h):
-    dev = _index(x, "x")
-    if x.dim() != 2:
-        _bad("x must be bfloat16 [M, K]")
+    dev = x.get_device()
     M, K = x.shape
-    bf16, device = torch.bfloat16, x.device
+    bf16 = torch.bfloat16
     ldx = _rows(x, "x", bf16, M, K, dev)
+    pw = _dense(weight, "weight", bf16, (K,), dev)
     ldq = ldr = ldro = ldh = K
     pr = pro = ph = None
     if q is None:
-        q = torch.empty(M, K, dtype=torch.uint8, device=device)
+        q = torch.empty((M, K), dtype=torch.uint8, device=x.device)
     else:
         ldq = _rows(q, "q", torch.uint8, M, K, dev)
     if residual is not None:
         ldr, pr = _rows(residual, "residual", bf16, M, K, dev), residual.data_ptr()
         if res_out is None:
-            res_out = torch.empty(M, K, dtype=bf16, device=device)
+            res_out = torch.empty((M, K), dtype=bf16, device=x.device)
             pro = res_out.data_ptr()
     if res_out is not None and pro is None:
         ldro, pro = _rows(res_out, "res_out", bf16, M, K, dev), res_out.data_ptr()
     if h is not None:
         ldh, ph = _rows(h, "h", bf16, M, K, dev), h.data_ptr()
     elif want_h:
-        h = torch.empty(M, K, dtype=bf16, device=device)
+        h = torch.empty((M, K), dtype=bf16, device=x.device)
         ph = h.data_ptr()
-    pw = _dense(weight, "weight", bf16, (K,), dev)
-    with _on(dev) as stream:
-        _check(fn(x.data_ptr(), ldx, pr, ldr, pw, weight_offset, eps, M, K, *group, q.data_ptr(),
-                  ldq, scales.data_ptr(), pro, ldro, ph, ldh, stream))
-    out = (q, scales)
-    if res_out is not None:
-        out += (res_out,)
-    return out if h is None else out + (h,)
+    _launch(fn, dev, x.data_ptr(), ldx, pr, ldr, pw, weight_offset, eps, M, K, *group,
+            q.data_ptr(), ldq, scales.data_ptr(), pro, ldro, ph, ldh)
+    if h is not None:
+        return (q, scales, h) if res_out is None else (q, scales, res_out, h)
+    return (q, scales) if res_out is None else (q, scales, res_out)
 
 
 def rmsnorm_quant(x, weight, eps=1e-6, residual=None, group_k=128, dtype=INT8, weight_offset=0.0,
@@ -651,7 +641,7 @@ def rmsnorm_quant(x, weight, eps=1e-6, residual=None, group_k=128, dtype=INT8, w
         _bad("group_k must be >= 1")
     M, K = x.shape
     if s is None:
-        s = torch.empty(-(-K // group_k), M, dtype=torch.float32, device=x.device)
+        s = torch.empty((-(-K // group_k), M), dtype=torch.float32, device=x.device)
     else:
         _dense(s, "s", torch.float32, (-(-K // group_k), M), dev)
     return _rmsnorm(lib().bq_rmsnorm_quant, x, weight, eps, residual, weight_offset, want_h,
@@ -667,11 +657,9 @@ def mx_rmsnorm_quant(x, weight, eps=1e-6, residual=None, weight_offset=0.0, want
     M, K = x.shape
     if sf is None:
         sf = torch.empty(mx_scale_bytes(M, K), dtype=torch.uint8, device=x.device)
-    else:
-        _there(sf, "sf", dev)
-        if sf.dtype is not torch.uint8 or not sf.is_contiguous() or \
-                sf.numel() < cdiv(M, 128) * (K // 128) * 512:
-            _bad(f"sf must be uint8, dense, of at least {mx_scale_bytes(M, K)} bytes")
+    elif sf.get_device() != dev or sf.dtype is not torch.uint8 or not sf.is_contiguous() or \
+            sf.numel() < -(-M // 128) * (K // 128) * 512:
+        _wrong(sf, "sf", torch.uint8, (mx_scale_bytes(M, K),), dev)
     return _rmsnorm(lib().bq_mx_rmsnorm_quant, x, weight, eps, residual, weight_offset, want_h,
                     (), q, sf, res_out, h)
 
@@ -690,12 +678,11 @@ def rope_frequencies(rot_dim, base=10000.0, scaling=ROPE_PLAIN, factor=1.0, orig
 
 def _heads(t, name: str, T: int, H: int, D: int, dev: int):
     """Token and head strides of a bf16 [T, H, D] tensor with unit last stride."""
-    _there(t, name, dev)
-    if t.dtype is not torch.bfloat16 or t.shape != (T, H, D):
-        _bad(f"{name} must be bfloat16 [{T}, {H}, {D}], not {t.dtype} {list(t.shape)}")
+    if t.get_device() != dev or t.dtype is not torch.bfloat16 or t.shape != (T, H, D):
+        _wrong(t, name, torch.bfloat16, (T, H, D), dev)
     st, sh, unit = t.stride()
     if unit != 1 and D > 1:
-        _bad(f"{name} must have unit stride in its last dimension")
+        _wrong(t, name, torch.bfloat16, (T, H, D), dev)
     return st, sh
 
 
@@ -704,23 +691,20 @@ def rope(x, positions, freqs, layout=ROPE_HALF, mscale=1.0, out=None):
     first 2 * len(freqs) dimensions of each head are turned, the rest copied.
     positions: int32 [T]; freqs, mscale: from rope_frequencies.  out may be x."""
     dev = _index(x, "x")
-    if x.dim() != 3:
-        _bad("x must be bfloat16 [T, H, D]")
+    if x.dim() != 3 or freqs.dim() != 1:
+        _bad("x must be bfloat16 [T, H, D], freqs float64 [rot_dim / 2]")
     T, H, D = x.shape
+    half = freqs.shape[0]
     xt, xh = _heads(x, "x", T, H, D, dev)
+    pp = _dense(positions, "positions", torch.int32, (T,), dev)
+    pf = _dense(freqs, "freqs", torch.float64, (half,), dev)
     if out is None:
-        out = torch.empty(T, H, D, dtype=torch.bfloat16, device=x.device)
+        out = torch.empty((T, H, D), dtype=torch.bfloat16, device=x.device)
         ot, oh = H * D, D
     else:
         ot, oh = _heads(out, "out", T, H, D, dev)
-    pp = _dense(positions, "positions", torch.int32, (T,), dev)
-    if freqs.dim() != 1:
-        _bad("freqs must be float64 [rot_dim / 2]")
-    half = freqs.shape[0]
-    pf = _dense(freqs, "freqs", torch.float64, (half,), dev)
-    with _on(dev) as stream:
-        _check(lib().bq_rope(x.data_ptr(), xt, xh, pp, pf, T, H, D, 2 * half, layout, mscale,
-                             out.data_ptr(), ot, oh, stream))
+    _launch(lib().bq_rope, dev, x.data_ptr(), xt, xh, pp, pf, T, H, D, 2 * half, layout, mscale,
+            out.data_ptr(), ot, oh)
     return out
 
 
@@ -786,9 +770,8 @@ def kv_append(cache: KvCache, k, v, seq_offsets, kv_lens, page_table):
     T = k.shape[0] if k.dim() else -1
     kt, kh = _heads(k, "k", T, H, D, dev)
     vt, vh = _heads(v, "v", T, H, D, dev)
-    with _on(dev) as stream:
-        _check(lib().bq_kv_append(k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, *batch, T, H, D, P,
-                                  page, bt, dtype, *ptrs, stream))
+    _launch(lib().bq_kv_append, dev, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, *batch, T, H, D,
+            P, page, bt, dtype, *ptrs)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -817,26 +800,22 @@ def kv_attention(q, cache: KvCache, seq_offsets, kv_lens, page_table, max_q_len,
     T, Hq = q.shape[0], q.shape[1]
     qt, qh = _heads(q, "q", T, Hq, D, dev)
     if out is None:
-        out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=q.device)
+        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
         ot, oh = Hq * D, D
     else:
         ot, oh = _heads(out, "out", T, Hq, D, dev)
     pl = None if lse is None else _dense(lse, "lse", torch.float32, (T, Hq), dev)
     need = kv_attention_workspace_size(batch[5], T, Hq, H, D, max_q_len, max_kv_len, page, bt)
-    pws = wsb = 0
-    if ws is not None:
-        _there(ws, "ws", dev)
-        if not ws.is_contiguous():
-            _bad("ws must be dense")
-    elif need:
-        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-    if ws is not None:
-        pws, wsb = ws.data_ptr(), ws.numel() * ws.element_size()
-    if scale is None:
-        scale = D ** -0.5
-    with _on(dev) as stream:
-        _check(lib().bq_kv_attention(
-            q.data_ptr(), qt, qh, *batch, T, Hq, H, D, max_q_len, max_kv_len, *ptrs, P, page, bt,
-            dtype, scale, 1 if causal else 0, window, out.data_ptr(), ot, oh, pl, pws, wsb,
-            stream))
+    if ws is None:
+        wsb = need
+        if need:
+            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+    else:
+        if ws.get_device() != dev or not ws.is_contiguous():
+            _wrong(ws, "ws", torch.uint8, (need,), dev)
+        wsb = ws.numel() * ws.element_size()
+    _launch(lib().bq_kv_attention, dev, q.data_ptr(), qt, qh, *batch, T, Hq, H, D, max_q_len,
+            max_kv_len, *ptrs, P, page, bt, dtype, D ** -0.5 if scale is None else scale,
+            1 if causal else 0, window, out.data_ptr(), ot, oh, pl,
+            None if ws is None else ws.data_ptr(), wsb)
     return out

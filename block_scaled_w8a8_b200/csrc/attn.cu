@@ -118,12 +118,18 @@ attn_merge_kernel(const AttnArgs a, const AttnParts p) {
       t >= s.row0 + s.n)
     return;                          // recorded by the kernel before, or nobody's row
   const float2* stat = reinterpret_cast<const float2*>(p.stat) + item * p.splits;
+  // the splits that hold keys this row sees
+  int lo, hi;
+  row_range(a, s, (int)(t - s.row0), lo, hi);
+  const int first = attn::first_split(a, s, p.chunk);
+  const int i0 = hi > lo ? lo / p.chunk - first : 0;
+  const int i1 = hi > lo ? (hi - 1) / p.chunk - first + 1 : 0;
   float mo = -INFINITY;
-  for (int i = lane; i < p.splits; i += 32) mo = fmaxf(mo, stat[i].y);
+  for (int i = i0 + lane; i < i1; i += 32) mo = fmaxf(mo, stat[i].y);
   mo = warp_max(mo);
   float l = 0.f, acc[kMaxD / 32] = {};
 #pragma unroll 4
-  for (int i = w; i < p.splits; i += NW) {
+  for (int i = i0 + w; i < i1; i += NW) {
     const float2 x = stat[i];
     if (x.x == 0.f) continue;
     const float f = attn::ex2(x.y - attn::finite(mo));
@@ -183,10 +189,15 @@ Path plan_path(int64_t D, int64_t page, int64_t rows) {
   return attn_decode_takes(D, page) ? Path::kDecode : Path::kAny;
 }
 
-int plan_splits(Path path, int64_t B, int64_t Hq, int64_t Hkv, int64_t max_q, int64_t max_kv) {
-  if (path == Path::kTc) return attn_tc_splits(B, Hkv, max_q, Hq / Hkv, max_kv);
-  if (path == Path::kDecode) return attn_decode_splits(B, Hkv, max_q * (Hq / Hkv), max_kv);
-  return 1;
+// Chunk of keys and most chunks that the keys of one sequence's rows lie in.
+void plan_splits(Path path, int64_t B, int64_t Hq, int64_t Hkv, int64_t max_q, int64_t max_kv,
+                 AttnParts& p) {
+  p.splits = 1;
+  p.chunk = 1 << 30;
+  const int64_t g = Hq / Hkv;
+  if (path == Path::kTc) p.chunk = attn_tc_chunk(B, Hkv, max_q, g, max_kv);
+  if (path == Path::kDecode) p.chunk = attn_decode_chunk(B, Hkv, max_q * g, max_kv);
+  p.splits = (int)std::max<int64_t>(1, (max_kv + p.chunk - 1) / p.chunk);
 }
 
 }  // namespace
@@ -194,8 +205,9 @@ int plan_splits(Path path, int64_t B, int64_t Hq, int64_t Hkv, int64_t max_q, in
 size_t attn_workspace_bytes(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
                             int64_t max_q, int64_t max_kv, int64_t page, int64_t bt) {
   (void)bt;
-  const Path path = plan_path(D, page, max_q * (Hq / Hkv));
-  return attn_part_bytes(T * Hq, plan_splits(path, B, Hq, Hkv, max_q, max_kv), D);
+  AttnParts p{};
+  plan_splits(plan_path(D, page, max_q * (Hq / Hkv)), B, Hq, Hkv, max_q, max_kv, p);
+  return attn_part_bytes(T * Hq, p.splits, D);
 }
 
 cudaError_t launch_attn_merge(const AttnArgs& a, const AttnParts& p, cudaStream_t st) {
@@ -211,7 +223,7 @@ cudaError_t launch_kv_attention(const AttnArgs& a, void* ws, cudaStream_t st) {
   const Path path = plan_path(a.c.D, a.c.page, (int64_t)a.max_q * (a.Hq / a.c.H));
   if (aligned && a.max_q > 0 && path != Path::kAny) {
     AttnParts p{};
-    p.splits = plan_splits(path, a.b.B, a.Hq, a.c.H, a.max_q, a.max_kv);
+    plan_splits(path, a.b.B, a.Hq, a.c.H, a.max_q, a.max_kv, p);
     if (p.splits > 1) {
       p.stat = static_cast<float*>(ws);
       p.o = p.stat + (2 * items * p.splits + 3) / 4 * 4;

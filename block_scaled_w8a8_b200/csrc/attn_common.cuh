@@ -32,14 +32,21 @@ __device__ __forceinline__ Range tile_range(const AttnArgs& a, const kv::Seq& s,
   return r;
 }
 
-// Part `split` of `splits` of the keys, cut at multiples of `step` from token
-// 0 on (so that no group of `step` tokens is shared); may be empty.
-__device__ __forceinline__ Range split_range(const Range& all, int split, int splits, int step) {
-  const int g0 = all.lo / step, g1 = (all.hi + step - 1) / step;
-  const int per = (max(g1 - g0, 0) + splits - 1) / splits;
+// Keys are split at the multiples of `chunk` tokens, counted from the one that
+// holds the first key any row of the sequence sees.
+__device__ __forceinline__ int first_split(const AttnArgs& a, const kv::Seq& s, int chunk) {
+  int lo, hi;
+  row_range(a, s, 0, lo, hi);
+  return lo / chunk;
+}
+
+// The keys of `all` in chunk number i; may be empty.  A chunk is a multiple of
+// the kernels' key tiles, and so is the start, but for that of `all` itself,
+// which is rounded down to the 128 keys of a tile.
+__device__ __forceinline__ Range split_range(const Range& all, int i, int chunk) {
   Range r;
-  r.lo = (int)min((int64_t)g1, g0 + (int64_t)split * per) * step;
-  r.hi = (int)min((int64_t)all.hi, min((int64_t)g1, g0 + ((int64_t)split + 1) * per) * step);
+  r.lo = (int)max((int64_t)all.lo / 128 * 128, (int64_t)i * chunk);
+  r.hi = (int)min((int64_t)all.hi, ((int64_t)i + 1) * chunk);
   return r;
 }
 

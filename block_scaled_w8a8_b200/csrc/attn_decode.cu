@@ -86,7 +86,8 @@ attn_decode_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles)
   // keys that some row of this tile sees, and this split's part of them
   const int i_lo = R0 / g, i_hi = min(s.n - 1, (R0 + R - 1) / g);
   const Range all = tile_range(a, s, i_lo, i_hi);
-  const Range part = split_range(all, split, parts.splits, 16 * NG);
+  const Range part = split_range(all, first_split(a, s, parts.chunk) + split, parts.chunk);
+  if (parts.splits > 1 && part.hi <= part.lo) return;      // the join does not look at it
 
   const int page = a.c.page, bt = a.c.bt, nblk = page / bt;
   const unsigned bt_inv = bt > 1 ? (unsigned)(0x100000000ull / (unsigned)bt + 1) : 0u;
@@ -445,13 +446,14 @@ bool attn_decode_takes(int64_t D, int64_t page) {
   return (D == 64 || D == 128) && page % 16 == 0;
 }
 
-// Enough CTAs to fill 148 SMs a few times over (sequences of different lengths
-// even out), but at least 256 keys for a CTA.
-int attn_decode_splits(int64_t B, int64_t Hkv, int64_t rows, int64_t max_kv) {
+// CTAs of at least 256 keys, and about sixteen for each of the 148 SMs where the
+// keys are enough for longer ones: a CTA's start and end cost as much as some
+// ten groups of 16 keys of a warp, but few long ones end unevenly (2 x up to
+// 131071 keys of dim 64: 8, 16, 24 CTAs an SM 73, 68, 78 us).
+int attn_decode_chunk(int64_t B, int64_t Hkv, int64_t rows, int64_t span) {
   const int64_t units = std::max<int64_t>(1, B * Hkv * ((rows + 15) / 16));
-  const int64_t want = (148 * 12 + units - 1) / units;
-  const int64_t most = std::max<int64_t>(1, max_kv / 256);
-  return (int)std::max<int64_t>(1, std::min<int64_t>({want, most, 256}));
+  const int64_t c = units * span / (148 * 16);
+  return (int)std::min<int64_t>(1 << 24, std::max<int64_t>(256, (c + 127) / 128 * 128));
 }
 
 cudaError_t launch_attn_decode(const AttnArgs& a, const AttnParts& p, cudaStream_t st) {

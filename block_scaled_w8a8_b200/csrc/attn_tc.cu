@@ -227,7 +227,8 @@ attn_tc_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles) {
   const bool two = R0 + BM < n_rows;      // the second row tile has rows
   const int i_lo = R0 / g, i_hi = min(s.n - 1, (R0 + 2 * BM - 1) / g);
   const Range all = tile_range(a, s, i_lo, i_hi);
-  const Range part = split_range(all, split, parts.splits, BN);
+  const Range part = split_range(all, first_split(a, s, parts.chunk) + split, parts.chunk);
+  if (parts.splits > 1 && part.hi <= part.lo) return;      // the join does not look at it
   const int keys = max(part.hi - part.lo, 0);
   const int nt = (keys + BN - 1) / BN, nb = (keys + SN - 1) / SN;   // key tiles, score blocks
 
@@ -742,11 +743,13 @@ int64_t attn_tc_tiles(int64_t max_q, int64_t group) {
 
 bool attn_tc_takes(int64_t D, int64_t page) { return (D == 64 || D == 128) && page % 16 == 0; }
 
-// One CTA runs on an SM: fill the 148, with at least 512 keys for a CTA.
-int attn_tc_splits(int64_t B, int64_t Hkv, int64_t max_q, int64_t group, int64_t max_kv) {
+// One CTA runs on an SM: keys are split where there are fewer CTAs than SMs, in
+// parts of at least 512.
+int attn_tc_chunk(int64_t B, int64_t Hkv, int64_t max_q, int64_t group, int64_t span) {
   const int64_t units = std::max<int64_t>(1, B * Hkv * attn_tc_tiles(max_q, group));
-  const int64_t most = std::max<int64_t>(1, max_kv / 512);
-  return (int)std::max<int64_t>(1, std::min<int64_t>({148 / units, most, 64}));
+  const int64_t parts = std::max<int64_t>(1, 148 / units);
+  if (parts == 1) return 1 << 30;
+  return (int)std::max<int64_t>(512, ((span + parts - 1) / parts + BN - 1) / BN * BN);
 }
 
 cudaError_t launch_attn_tc(const AttnArgs& a, const AttnParts& p, cudaStream_t st) {
