@@ -15,7 +15,6 @@ Layouts (see include/bq.h):
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 import threading
 from typing import NamedTuple
@@ -539,92 +538,31 @@ def moe_combine(y, inv_perm, topk_w, out=None):
 
 
 # ---- between two linears: norm, rotary positions, cache, attention ----------
-# These calls are short kernels in a decoding step, so their checks are kept
-# cheap: device indices, no message formatted unless it is raised.
+# These calls are short kernels in a decoding step, so their checks and their
+# marshalling are native (csrc/torch_calls.cpp); what follows names the arguments.
 
-def _bad(msg: str):
-    raise ValueError(msg)
-
-
-def _index(t, name: str) -> int:
-    """The index of t's CUDA device (raises for anything else)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    i = t.get_device()
-    if i < 0:
-        raise ValueError(f"{name} must be on a CUDA device (libbq has no CPU path)")
-    return i
+_calls = None
 
 
-def _wrong(t, name: str, dtype, shape, dev: int):
-    """Raises for what the checks below found wrong with t."""
-    if _index(t, name) != dev:
-        _bad(f"{name} must be on cuda:{dev}, not {t.device}")
-    _bad(f"{name} must be {dtype} {list(shape)}, with dense rows that do not overlap, not "
-         f"{t.dtype} {list(t.shape)} with strides {t.stride()}")
+def _load_calls():
+    """The extension module _torch_calls (raises if it has not been built)."""
+    global _calls
+    lib()
+    try:
+        from . import _torch_calls
+    except ImportError as e:
+        raise RuntimeError(
+            f"{os.path.join(os.path.dirname(LIB_PATH), '_torch_calls.so')} is missing or does not "
+            f"fit this torch ({e}): build it with `python -m block_scaled_w8a8_b200.build`") from e
+    _calls = _torch_calls
+    return _calls
 
 
-def _rows(t, name: str, dtype, M: int, K: int, dev: int) -> int:
-    """Row stride of a [M, K] tensor of `dtype` with unit column stride."""
-    if t.get_device() != dev or t.dtype is not dtype or t.shape != (M, K):
-        _wrong(t, name, dtype, (M, K), dev)
-    ld, unit = t.stride()
-    if (unit != 1 and K > 1) or (ld < K and M > 1):
-        _wrong(t, name, dtype, (M, K), dev)
-    return ld if ld > K else K
-
-
-def _dense(t, name: str, dtype, shape: tuple, dev: int) -> int:
-    """Address of a dense tensor of that shape."""
-    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape or \
-            not t.is_contiguous():
-        _wrong(t, name, dtype, shape, dev)
-    return t.data_ptr()
-
-
-_cuda_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
-
-
-def _launch(fn, dev: int, *args):
-    """fn(*args, stream) with `dev` as the current device; its current stream."""
-    if _cuda_device() == dev:
-        status = fn(*args, _raw_stream(dev))
-    else:
-        with torch.cuda.device(dev):
-            status = fn(*args, _raw_stream(dev))
-    if status:
-        _check(status)
-
-
-def _rmsnorm(fn, x, weight, eps, residual, weight_offset, want_h, group, q, scales, res_out, h):
-    dev = x.get_device()
-    M, K = x.shape
-    bf16 = torch.bfloat16
-    ldx = _rows(x, "x", bf16, M, K, dev)
-    pw = _dense(weight, "weight", bf16, (K,), dev)
-    ldq = ldr = ldro = ldh = K
-    pr = pro = ph = None
-    if q is None:
-        q = torch.empty((M, K), dtype=torch.uint8, device=x.device)
-    else:
-        ldq = _rows(q, "q", torch.uint8, M, K, dev)
-    if residual is not None:
-        ldr, pr = _rows(residual, "residual", bf16, M, K, dev), residual.data_ptr()
-        if res_out is None:
-            res_out = torch.empty((M, K), dtype=bf16, device=x.device)
-            pro = res_out.data_ptr()
-    if res_out is not None and pro is None:
-        ldro, pro = _rows(res_out, "res_out", bf16, M, K, dev), res_out.data_ptr()
-    if h is not None:
-        ldh, ph = _rows(h, "h", bf16, M, K, dev), h.data_ptr()
-    elif want_h:
-        h = torch.empty((M, K), dtype=bf16, device=x.device)
-        ph = h.data_ptr()
-    _launch(fn, dev, x.data_ptr(), ldx, pr, ldr, pw, weight_offset, eps, M, K, *group,
-            q.data_ptr(), ldq, scales.data_ptr(), pro, ldro, ph, ldh)
-    if h is not None:
-        return (q, scales, h) if res_out is None else (q, scales, res_out, h)
-    return (q, scales) if res_out is None else (q, scales, res_out)
+def _done(result):
+    """A native call's result; an int is the status of a call that libbq refused."""
+    if type(result) is int:
+        _check(result)
+    return result
 
 
 def rmsnorm_quant(x, weight, eps=1e-6, residual=None, group_k=128, dtype=INT8, weight_offset=0.0,
@@ -634,34 +572,15 @@ def rmsnorm_quant(x, weight, eps=1e-6, residual=None, group_k=128, dtype=INT8, w
     x, residual: bf16 [M, K]; weight: bf16 [K].  Returns (q [M, K], s [Kb, M]),
     then res_out = bf16(x + residual) if there is a residual (or res_out is
     given), then h = bf16(y) if want_h.  res_out may be residual or x."""
-    dev = _index(x, "x")
-    if x.dim() != 2:
-        _bad("x must be bfloat16 [M, K]")
-    if group_k < 1:
-        _bad("group_k must be >= 1")
-    M, K = x.shape
-    if s is None:
-        s = torch.empty((-(-K // group_k), M), dtype=torch.float32, device=x.device)
-    else:
-        _dense(s, "s", torch.float32, (-(-K // group_k), M), dev)
-    return _rmsnorm(lib().bq_rmsnorm_quant, x, weight, eps, residual, weight_offset, want_h,
-                    (group_k, dtype), q, s, res_out, h)
+    return _done((_calls or _load_calls()).rmsnorm(
+        x, weight, eps, residual, group_k, dtype, weight_offset, want_h, q, s, res_out, h, False))
 
 
 def mx_rmsnorm_quant(x, weight, eps=1e-6, residual=None, weight_offset=0.0, want_h=False, q=None,
                      sf=None, res_out=None, h=None):
     """rmsnorm_quant with MXFP8 codes and scale atoms, for mx_gemm."""
-    dev = _index(x, "x")
-    if x.dim() != 2:
-        _bad("x must be bfloat16 [M, K]")
-    M, K = x.shape
-    if sf is None:
-        sf = torch.empty(mx_scale_bytes(M, K), dtype=torch.uint8, device=x.device)
-    elif sf.get_device() != dev or sf.dtype is not torch.uint8 or not sf.is_contiguous() or \
-            sf.numel() < -(-M // 128) * (K // 128) * 512:
-        _wrong(sf, "sf", torch.uint8, (mx_scale_bytes(M, K),), dev)
-    return _rmsnorm(lib().bq_mx_rmsnorm_quant, x, weight, eps, residual, weight_offset, want_h,
-                    (), q, sf, res_out, h)
+    return _done((_calls or _load_calls()).rmsnorm(
+        x, weight, eps, residual, 32, FP8_E4M3, weight_offset, want_h, q, sf, res_out, h, True))
 
 
 def rope_frequencies(rot_dim, base=10000.0, scaling=ROPE_PLAIN, factor=1.0, orig_max_pos=0,
@@ -676,36 +595,11 @@ def rope_frequencies(rot_dim, base=10000.0, scaling=ROPE_PLAIN, factor=1.0, orig
     return host.to(device), ms.value
 
 
-def _heads(t, name: str, T: int, H: int, D: int, dev: int):
-    """Token and head strides of a bf16 [T, H, D] tensor with unit last stride."""
-    if t.get_device() != dev or t.dtype is not torch.bfloat16 or t.shape != (T, H, D):
-        _wrong(t, name, torch.bfloat16, (T, H, D), dev)
-    st, sh, unit = t.stride()
-    if unit != 1 and D > 1:
-        _wrong(t, name, torch.bfloat16, (T, H, D), dev)
-    return st, sh
-
-
 def rope(x, positions, freqs, layout=ROPE_HALF, mscale=1.0, out=None):
     """Rotary positions on bf16 x [T, H, D] (any token and head strides): the
     first 2 * len(freqs) dimensions of each head are turned, the rest copied.
     positions: int32 [T]; freqs, mscale: from rope_frequencies.  out may be x."""
-    dev = _index(x, "x")
-    if x.dim() != 3 or freqs.dim() != 1:
-        _bad("x must be bfloat16 [T, H, D], freqs float64 [rot_dim / 2]")
-    T, H, D = x.shape
-    half = freqs.shape[0]
-    xt, xh = _heads(x, "x", T, H, D, dev)
-    pp = _dense(positions, "positions", torch.int32, (T,), dev)
-    pf = _dense(freqs, "freqs", torch.float64, (half,), dev)
-    if out is None:
-        out = torch.empty((T, H, D), dtype=torch.bfloat16, device=x.device)
-        ot, oh = H * D, D
-    else:
-        ot, oh = _heads(out, "out", T, H, D, dev)
-    _launch(lib().bq_rope, dev, x.data_ptr(), xt, xh, pp, pf, T, H, D, 2 * half, layout, mscale,
-            out.data_ptr(), ot, oh)
-    return out
+    return _done((_calls or _load_calls()).rope(x, positions, freqs, layout, mscale, out))
 
 
 class KvCache(NamedTuple):
@@ -721,7 +615,7 @@ class KvCache(NamedTuple):
 def kv_cache(n_pages, n_heads, page_size, head_dim, block_t=16, dtype=INT8, device="cuda"):
     """An empty cache."""
     if block_t < 1 or page_size % block_t:
-        _bad("block_t must divide page_size")
+        raise ValueError("block_t must divide page_size")
     codes = [torch.zeros(n_pages, n_heads, page_size, head_dim, dtype=torch.uint8, device=device)
              for _ in range(2)]
     scales = [torch.zeros(n_pages, n_heads, page_size // block_t, dtype=torch.float32,
@@ -729,52 +623,14 @@ def kv_cache(n_pages, n_heads, page_size, head_dim, block_t=16, dtype=INT8, devi
     return KvCache(*codes, *scales, dtype)
 
 
-def _cache_args(k, v, ks, vs, dev: int):
-    """(n_pages, Hkv, page_size, D, block_t) and the four addresses."""
-    if k.dim() != 4 or ks.dim() != 3:
-        _bad("cache codes must be uint8 [n_pages, Hkv, page_size, D], scales float32 "
-             "[n_pages, Hkv, page_size / block_t]")
-    shape = k.shape
-    n_pages, H, page, D = shape
-    blocks = ks.shape[2]
-    sshape = (n_pages, H, blocks)
-    ptrs = (_dense(k, "cache.k", torch.uint8, shape, dev),
-            _dense(v, "cache.v", torch.uint8, shape, dev),
-            _dense(ks, "cache.ks", torch.float32, sshape, dev),
-            _dense(vs, "cache.vs", torch.float32, sshape, dev))
-    if page < 1 or blocks < 1 or page % blocks:
-        _bad("block_t must divide page_size")
-    return n_pages, H, page, D, page // blocks, ptrs
-
-
-def _batch_args(seq_offsets, kv_lens, page_table, dev: int):
-    """(offsets, lengths, table, ld_table, table_cols, B)."""
-    if kv_lens.dim() != 1 or page_table.dim() != 2:
-        _bad("kv_lens must be int32 [B], page_table int32 [B, pages]")
-    B = kv_lens.shape[0]
-    lens = _dense(kv_lens, "kv_lens", torch.int32, (B,), dev)
-    off = _dense(seq_offsets, "seq_offsets", torch.int32, (B + 1,), dev)
-    ld = _rows(page_table, "page_table", torch.int32, B, page_table.shape[1], dev)
-    return off, lens, page_table.data_ptr(), ld, page_table.shape[1], B
-
-
 def kv_append(cache: KvCache, k, v, seq_offsets, kv_lens, page_table):
     """Quantise the new tokens' keys and values, bf16 [T, Hkv, D] (any token and
     head strides), into the cache.  Rows seq_offsets[b] .. seq_offsets[b+1] are
     the last tokens of sequence b, whose length with them is kv_lens[b];
     page_table int32 [B, pages].  Lengths and pages are read on the device."""
-    dev = _index(k, "k")
-    ck, cv, cks, cvs, dtype = cache
-    P, H, page, D, bt, ptrs = _cache_args(ck, cv, cks, cvs, dev)
-    batch = _batch_args(seq_offsets, kv_lens, page_table, dev)
-    T = k.shape[0] if k.dim() else -1
-    kt, kh = _heads(k, "k", T, H, D, dev)
-    vt, vh = _heads(v, "v", T, H, D, dev)
-    _launch(lib().bq_kv_append, dev, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, *batch, T, H, D,
-            P, page, bt, dtype, *ptrs)
+    _done((_calls or _load_calls()).kv_append(*cache, k, v, seq_offsets, kv_lens, page_table))
 
 
-@functools.lru_cache(maxsize=1024)
 def kv_attention_workspace_size(B, T, Hq, Hkv, D, max_q_len, max_kv_len, page_size,
                                 block_t) -> int:
     n = ctypes.c_size_t(0)
@@ -791,31 +647,6 @@ def kv_attention(q, cache: KvCache, seq_offsets, kv_lens, page_table, max_q_len,
     a causal row sees, 0 for all.  lse: float32 [T, Hq] to fill, or None.
     Rows at and behind seq_offsets[B] are left as they are.  Without ws, the
     workspace is allocated for the call."""
-    dev = _index(q, "q")
-    ck, cv, cks, cvs, dtype = cache
-    P, H, page, D, bt, ptrs = _cache_args(ck, cv, cks, cvs, dev)
-    batch = _batch_args(seq_offsets, kv_lens, page_table, dev)
-    if q.dim() != 3:
-        _bad("q must be bfloat16 [T, Hq, D]")
-    T, Hq = q.shape[0], q.shape[1]
-    qt, qh = _heads(q, "q", T, Hq, D, dev)
-    if out is None:
-        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
-        ot, oh = Hq * D, D
-    else:
-        ot, oh = _heads(out, "out", T, Hq, D, dev)
-    pl = None if lse is None else _dense(lse, "lse", torch.float32, (T, Hq), dev)
-    need = kv_attention_workspace_size(batch[5], T, Hq, H, D, max_q_len, max_kv_len, page, bt)
-    if ws is None:
-        wsb = need
-        if need:
-            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-    else:
-        if ws.get_device() != dev or not ws.is_contiguous():
-            _wrong(ws, "ws", torch.uint8, (need,), dev)
-        wsb = ws.numel() * ws.element_size()
-    _launch(lib().bq_kv_attention, dev, q.data_ptr(), qt, qh, *batch, T, Hq, H, D, max_q_len,
-            max_kv_len, *ptrs, P, page, bt, dtype, D ** -0.5 if scale is None else scale,
-            1 if causal else 0, window, out.data_ptr(), ot, oh, pl,
-            None if ws is None else ws.data_ptr(), wsb)
-    return out
+    return _done((_calls or _load_calls()).kv_attention(
+        q, *cache, seq_offsets, kv_lens, page_table, max_q_len, max_kv_len, scale, causal, window,
+        out, lse, ws))

@@ -1,8 +1,10 @@
-"""Build libbq.so (the C-ABI CUDA library) in-tree for sm_100a.
+"""Build libbq.so (the C-ABI CUDA library) in-tree for sm_100a, and the
+extension module _torch_calls.so that calls it on torch tensors.
 
 Each csrc/*.cu file is compiled by nvcc (in parallel) into _build/, then
 linked into block_scaled_w8a8_b200/libbq.so with the CUDA runtime linked
-statically, so the library loads on hosts without a GPU.
+statically, so the library loads on hosts without a GPU.  csrc/torch_calls.cpp
+is compiled by the host compiler against torch's headers and linked to libbq.so.
 
     python -m block_scaled_w8a8_b200.build [--force] [--verbose-ptxas]
 """
@@ -14,12 +16,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libbq.so")
+EXT = os.path.join(PKG, "_torch_calls.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 # No fast-math, no flush-to-zero: quantisation must round like IEEE fp32.
@@ -59,12 +63,43 @@ def _compile(src: str, verbose_ptxas: bool) -> str:
     return obj
 
 
+def _compile_ext() -> str:
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    obj = os.path.join(BUILD, "torch_calls.o")
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"],
+           "-isystem", os.path.join(cuda, "include"), "-I" + os.path.join(ROOT, "include"),
+           "-c", os.path.join(CSRC, "torch_calls.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compiling torch_calls.cpp failed:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_ext(obj: str):
+    import torch
+    tmp = EXT + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, "-L" + PKG, "-l:libbq.so",
+           "-L" + os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python",
+           "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"linking _torch_calls failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, EXT)
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime():
+    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _deps_mtime()
+                         for f in (LIB, EXT)):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
+        ext = ex.submit(_compile_ext)
         objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), srcs))
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
@@ -72,6 +107,7 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_ext(ext.result())
     return LIB
 
 
