@@ -60,7 +60,7 @@ struct Place {
 
 // UNI: block_t is a multiple of 16, so that the group shares its scales.
 template <int DT, int D, int NR, bool UNI>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kWarps * 32, NR == 1 ? 4 : 2)
 attn_decode_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles) {
   constexpr int NG = 128 / D;              // groups of 16 tokens in flight: 4 KB of codes a warp
   constexpr int KS = D / 16;               // k-steps of the score product
@@ -75,7 +75,28 @@ attn_decode_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles)
   const int split = (int)(blockIdx.x % (unsigned)parts.splits);
   const int bt_ = (int)(blockIdx.x / (unsigned)parts.splits);
   const int rt = bt_ % row_tiles, b = bt_ / row_tiles, hk = blockIdx.y;
-  const int g = a.Hq / a.c.H;
+  const int g = a.Hq / a.c.H, page = a.c.page;
+  const int32_t* table = a.b.table + (int64_t)b * a.b.ld_table;
+  constexpr int STEP = 16 * NG, STRIDE = kWarps * STEP;
+  // without a window a split begins at a place known beforehand: its first pages
+  // are asked for together with the sequence's length
+  Place at[2][NG];                         // of the next two rounds' groups
+  int32_t pg[2][NG];                       // their pages
+  auto pages = [&](int t, int end) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int u = 0; u < NG; ++u) {
+        const int64_t tu = (int64_t)t + h * STRIDE + 16 * u;
+        const int idx = (int)(tu / page);
+        at[h][u] = {idx, (int)(tu - (int64_t)idx * page)};
+        pg[h][u] = tu < end ? table[idx] : -1;
+      }
+  };
+  const int64_t guess = (int64_t)split * parts.chunk + warp * STEP;
+  const int held = a.b.table_cols * page;
+  const bool early = a.window == 0 && guess < held;
+  if (early) pages((int)guess, held);
   kv::Seq s;
   if (!kv::load_seq(a.b, a.c.page, b, s) || s.n > a.max_q || s.len > a.max_kv) {
     if (threadIdx.x == 0) record_status(a.status, kStatusBadInput, 0x711u);
@@ -89,31 +110,25 @@ attn_decode_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles)
   const Range part = split_range(all, first_split(a, s, parts.chunk) + split, parts.chunk);
   if (parts.splits > 1 && part.hi <= part.lo) return;      // the join does not look at it
 
-  const int page = a.c.page, bt = a.c.bt, nblk = page / bt;
+  const int bt = a.c.bt, nblk = page / bt;
   const unsigned bt_inv = bt > 1 ? (unsigned)(0x100000000ull / (unsigned)bt + 1) : 0u;
-  constexpr int STEP = 16 * NG, STRIDE = kWarps * STEP;
   const int stride_idx = STRIDE / page, stride_slot = STRIDE % page;
-  const int32_t* table = a.b.table + (int64_t)b * a.b.ld_table;
   const uint8_t* kbase = a.c.k + r * D + 16 * c;
   const uint8_t* vbase = a.c.v + 2 * c * D + r * (D / 8);
   int t = part.lo + warp * STEP;
-  Place at[NG];                            // of the groups whose page is to be fetched next
-  int32_t pg[NG];                          // page of the groups to be loaded next
-#pragma unroll
-  for (int u = 0; u < NG; ++u) {
-    const int tu = t + 16 * u;
-    at[u].idx = tu / page;
-    at[u].slot = tu - at[u].idx * page;
-    pg[u] = tu < part.hi ? table[at[u].idx] : -1;
-  }
-  // page and slot of a group -> first code row and scale, or -1
-  auto row_of = [&](int u) -> int64_t {
-    return pg[u] >= 0 && (int64_t)pg[u] < a.c.n_pages ? (int64_t)pg[u] * a.c.H + hk : -1;
+  if (!early) pages(t, part.hi);
+  // (page, key head) of the next round's group u, which begins at token tok, or -1
+  auto row_of = [&](int u, int tok) -> int64_t {
+    if (tok >= part.hi) return -1;
+    const int64_t p = pg[0][u];
+    if (p >= 0 && p < a.c.n_pages) return p * a.c.H + hk;
+    if (lane == 0) record_status(a.status, kStatusBadInput, 0x712u);
+    return -1;
   };
   Group<D, UNI> G[NG];
   bool ok[NG];                             // the group's page exists (warp-uniform)
   auto load_k = [&](int u, int64_t ph) {
-    const int slot = at[u].slot;
+    const int slot = at[0][u].slot;
     if (ph < 0) return;
     const uint8_t* p = kbase + (ph * page + slot) * D;
 #pragma unroll
@@ -127,7 +142,7 @@ attn_decode_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles)
     }
   };
   auto load_v = [&](int u, int64_t ph) {
-    const int slot = at[u].slot;
+    const int slot = at[0][u].slot;
     if (ph < 0) return;
     const uint8_t* p = vbase + (ph * page + slot) * D;
 #pragma unroll
@@ -141,12 +156,10 @@ attn_decode_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles)
   int64_t ph[NG];
 #pragma unroll
   for (int u = 0; u < NG; ++u) {
-    ph[u] = row_of(u);
+    ph[u] = row_of(u, t + 16 * u);
     ok[u] = ph[u] >= 0;
     load_k(u, ph[u]);
     load_v(u, ph[u]);
-    if (!ok[u] && t + 16 * u < part.hi && lane == 0)
-      record_status(a.status, kStatusBadInput, 0x712u);
   }
 
   // queries: row R0 + 8 nt + r of lane (r, c), dims 64 i + 16 c .. + 15
@@ -213,16 +226,18 @@ attn_decode_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles)
   }
 
   for (; t < part.hi; t += STRIDE) {
-    // the next groups' pages
+    // the next round's pages are here; those of the one after it are asked for
 #pragma unroll
     for (int u = 0; u < NG; ++u) {
-      at[u].idx += stride_idx;
-      at[u].slot += stride_slot;
-      if (at[u].slot >= page) {
-        at[u].slot -= page;
-        ++at[u].idx;
+      at[0][u] = at[1][u];
+      pg[0][u] = pg[1][u];
+      at[1][u].idx += stride_idx;
+      at[1][u].slot += stride_slot;
+      if (at[1][u].slot >= page) {
+        at[1][u].slot -= page;
+        ++at[1][u].idx;
       }
-      pg[u] = t + STRIDE + 16 * u < part.hi ? table[at[u].idx] : -1;
+      pg[1][u] = (int64_t)t + 2 * STRIDE + 16 * u < part.hi ? table[at[1][u].idx] : -1;
     }
     bool whole = t >= in_lo && t + STEP <= in_hi;
 #pragma unroll
@@ -265,9 +280,7 @@ attn_decode_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles)
     int64_t ph_next[NG];
 #pragma unroll
     for (int u = 0; u < NG; ++u) {
-      ph_next[u] = row_of(u);
-      if (ph_next[u] < 0 && t + STRIDE + 16 * u < part.hi && lane == 0)
-        record_status(a.status, kStatusBadInput, 0x712u);
+      ph_next[u] = row_of(u, t + STRIDE + 16 * u);
       load_k(u, ph_next[u]);
     }
     if (!whole) {

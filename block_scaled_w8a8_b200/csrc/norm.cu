@@ -130,14 +130,16 @@ __global__ void __launch_bounds__(kAnyThreads) norm_any_kernel(const NormArgs a)
 // Rows of whole 16-byte vectors, groups of 8 lanes' worth of a power of two (or
 // the whole row): a CTA per row, V vectors of 8 elements a thread, everything in
 // registers, one barrier a row.  Memory-bound: x and the residual are read once,
-// the sum, the codes and the scales written once.
+// the sum, the codes and the scales written once; the next row is under way while
+// one is reduced.  In place is safe: a row is loaded and stored by one CTA, each
+// element by one thread, loads first.
 //
 // Codes are formed with the reciprocal of the scale: y itself is only good to an
 // fp32 rounding, and one more of those moves a code only where y / s lies within
 // that of a border.  INT8: fma(y, 1/s, 1.5 * 2^23) rounds to nearest even and
 // leaves the code in the low byte, with no conversion unit involved.
 template <int DT, int V>
-__global__ void __launch_bounds__(V == 1 ? 1024 : 512)
+__global__ void __launch_bounds__(V <= 2 ? 1024 : 512)
 norm_vec_kernel(const NormArgs a, const int lpg) {       // lpg: lanes of a group, 0 = the row
   __shared__ float red[2][2][32];
   asm volatile("griddepcontrol.launch_dependents;");
@@ -151,20 +153,30 @@ norm_vec_kernel(const NormArgs a, const int lpg) {       // lpg: lanes of a grou
     const int v = i * nt + tid;
     wv[i] = v < nvec ? __ldg(reinterpret_cast<const uint4*>(a.w) + v) : make_uint4(0u, 0u, 0u, 0u);
   }
-  int parity = 0;
-  for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x, parity ^= 1) {
+  uint4 nx[V], ns[V];                       // the next row, under way while this one is reduced
+  auto load = [&](int64_t m) {
     const uint4* x = reinterpret_cast<const uint4*>(a.x + m * a.ldx);
     const uint4* res = reinterpret_cast<const uint4*>(a.res + m * a.ldr);
-    uint4 rv[V], sv[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int v = i * nt + tid;
-      rv[i] = sv[i] = make_uint4(0u, 0u, 0u, 0u);
+      nx[i] = ns[i] = make_uint4(0u, 0u, 0u, 0u);
       if (v < nvec) {
-        rv[i] = x[v];
-        if (a.res) sv[i] = res[v];
+        nx[i] = x[v];
+        if (a.res) ns[i] = res[v];
       }
     }
+  };
+  if (blockIdx.x < a.M) load(blockIdx.x);
+  int parity = 0;
+  for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x, parity ^= 1) {
+    uint4 rv[V], sv[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      rv[i] = nx[i];
+      sv[i] = ns[i];
+    }
+    if (m + gridDim.x < a.M) load(m + gridDim.x);
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -266,7 +278,7 @@ template <int DT, int V>
 cudaError_t launch_vec(const NormArgs& a, cudaStream_t st) {
   const int64_t nvec = a.K / 8;
   const int nt = (int)((nvec + 32 * V - 1) / (32 * V)) * 32;
-  const int64_t fit = std::max(1, 2048 / nt);            // CTAs of an SM, by its threads
+  const int64_t fit = std::max(1, 1024 / nt);            // CTAs of an SM: 64 registers a thread
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)std::min<int64_t>(a.M, 148 * fit));
   cfg.blockDim = dim3((unsigned)nt);
@@ -306,7 +318,7 @@ cudaError_t launch_dt(const NormArgs& a, cudaStream_t st) {
   // few rows: a vector a thread, for latency; many: more loads in flight a thread
   if (a.M <= 148 && a.K <= 8192) return launch_vec<DT, 1>(a, st);
   if (a.K <= 2048) return launch_vec<DT, 1>(a, st);
-  return a.K <= 16384 ? launch_vec<DT, 4>(a, st) : launch_vec<DT, 8>(a, st);
+  return a.K <= 16384 ? launch_vec<DT, 2>(a, st) : launch_vec<DT, 8>(a, st);
 }
 
 }  // namespace

@@ -90,45 +90,61 @@ __global__ void __launch_bounds__(kVecThreads) rope_vec_kernel(const RopeArgs a,
     cs[e] = make_float2(c, sn);
   }
   __syncthreads();
-  // vectors of a head: those with pairs, then those that are copied
+  // vectors of a head: those with pairs, then those that are copied; a thread has
+  // the same one of all its heads, so its sines and cosines are read once a token
   const int np = INTER ? (int)a.rot / 8 : half / 8;
   const int nc = a.out == a.x ? 0 : (int)(a.D - a.rot) / 8, per = np + nc;
-  const int total = nt * H * per;
-  for (int i = tid; i < total; i += kVecThreads) {
-    const int th = i / per, e = i - th * per, t = th / H, h = th - t * H;
-    const uint16_t* x = a.x + (t0 + t) * a.ldt + h * a.ldh;
-    uint16_t* o = a.out + (t0 + t) * a.ldot + h * a.ldoh;
-    if (e >= np) {
-      const int64_t d = a.rot + 8 * (e - np);
-      *reinterpret_cast<uint4*>(o + d) = *reinterpret_cast<const uint4*>(x + d);
-      continue;
+  const int lanes = kVecThreads / per;            // heads side by side
+  const int e = tid % per, h0 = tid / per;
+  if (h0 >= lanes) return;
+  const bool copy = e >= np;
+  const int64_t at = copy ? a.rot + 8 * (e - np) : 8 * e;
+  // kBatch heads at a time: all their loads before the first store, which may be
+  // to the same buffer (every element is read and written by one thread)
+  constexpr int kBatch = INTER ? 6 : 4;
+  for (int t = 0; t < nt; ++t) {
+    const uint16_t* xt = a.x + (t0 + t) * a.ldt + at;
+    uint16_t* ot = a.out + (t0 + t) * a.ldot + at;
+    float4 f[INTER ? 2 : 4];
+    if (!copy) {
+#pragma unroll
+      for (int k = 0; k < (INTER ? 2 : 4); ++k)
+        f[k] = reinterpret_cast<const float4*>(cs + t * half + (INTER ? 4 : 8) * e)[k];
     }
-    const float4* f = reinterpret_cast<const float4*>(cs + t * half + (INTER ? 4 : 8) * e);
-    if (INTER) {
-      uint4 v = *reinterpret_cast<const uint4*>(x + 8 * e);
-      uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+    for (int hb = h0; hb < H; hb += kBatch * lanes) {
+      uint4 va[kBatch], vb[INTER ? 1 : kBatch];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float4 q = f[k >> 1];
-        const float c = k & 1 ? q.z : q.x, s = k & 1 ? q.w : q.y;
-        const float p = __uint_as_float(w[k] << 16), r = __uint_as_float(w[k] & 0xFFFF0000u);
-        w[k] = pack_bf16(turned_a(p, r, c, s), turned_b(p, r, c, s));
+      for (int i = 0; i < kBatch; ++i) {
+        const int h = hb + i * lanes;
+        if (h >= H) break;
+        va[i] = *reinterpret_cast<const uint4*>(xt + h * a.ldh);
+        if (!INTER && !copy) vb[INTER ? 0 : i] = *reinterpret_cast<const uint4*>(xt + h * a.ldh + half);
       }
-      *reinterpret_cast<uint4*>(o + 8 * e) = v;
-    } else {
-      uint4 va = *reinterpret_cast<const uint4*>(x + 8 * e);
-      uint4 vb = *reinterpret_cast<const uint4*>(x + half + 8 * e);
-      uint32_t *wa = reinterpret_cast<uint32_t*>(&va), *wb = reinterpret_cast<uint32_t*>(&vb);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float4 q = f[k];
-        const float a0 = __uint_as_float(wa[k] << 16), a1 = __uint_as_float(wa[k] & 0xFFFF0000u);
-        const float b0 = __uint_as_float(wb[k] << 16), b1 = __uint_as_float(wb[k] & 0xFFFF0000u);
-        wa[k] = pack_bf16(turned_a(a0, b0, q.x, q.y), turned_a(a1, b1, q.z, q.w));
-        wb[k] = pack_bf16(turned_b(a0, b0, q.x, q.y), turned_b(a1, b1, q.z, q.w));
+      for (int i = 0; i < kBatch; ++i) {
+        const int h = hb + i * lanes;
+        if (h >= H) break;
+        uint32_t* wa = reinterpret_cast<uint32_t*>(&va[i]);
+        uint32_t* wb = reinterpret_cast<uint32_t*>(&vb[INTER ? 0 : i]);
+        if (!copy) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float4 q = f[INTER ? k >> 1 : k];
+            const float a0 = __uint_as_float(wa[k] << 16), a1 = __uint_as_float(wa[k] & 0xFFFF0000u);
+            if (INTER) {
+              const float c = k & 1 ? q.z : q.x, s = k & 1 ? q.w : q.y;
+              wa[k] = pack_bf16(turned_a(a0, a1, c, s), turned_b(a0, a1, c, s));
+            } else {
+              const float b0 = __uint_as_float(wb[k] << 16);
+              const float b1 = __uint_as_float(wb[k] & 0xFFFF0000u);
+              wa[k] = pack_bf16(turned_a(a0, b0, q.x, q.y), turned_a(a1, b1, q.z, q.w));
+              wb[k] = pack_bf16(turned_b(a0, b0, q.x, q.y), turned_b(a1, b1, q.z, q.w));
+            }
+          }
+          if (!INTER) *reinterpret_cast<uint4*>(ot + h * a.ldoh + half) = vb[INTER ? 0 : i];
+        }
+        *reinterpret_cast<uint4*>(ot + h * a.ldoh) = va[i];
       }
-      *reinterpret_cast<uint4*>(o + 8 * e) = va;
-      *reinterpret_cast<uint4*>(o + half + 8 * e) = vb;
     }
   }
 }
@@ -137,7 +153,7 @@ bool vec_ok(const RopeArgs& a) {
   auto al = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
   const int64_t unit = a.interleaved ? 8 : 16;           // of rot
   return al(a.x) && al(a.out) && a.ldt % 8 == 0 && a.ldh % 8 == 0 && a.ldot % 8 == 0 &&
-         a.ldoh % 8 == 0 && a.D % 8 == 0 && a.rot % unit == 0 && a.rot <= 1024 &&
+         a.ldoh % 8 == 0 && a.D % 8 == 0 && a.rot % unit == 0 && a.D <= 1024 && a.D >= 8 && (a.rot > 0 || a.out != a.x) &&
          a.H * a.D <= (1 << 22);
 }
 
@@ -155,8 +171,8 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st) {
   if (vec_ok(a)) {
     // many tokens: as many a CTA as one round of its threads has angles for
     const int64_t half = std::max<int64_t>(1, a.rot / 2);
-    int64_t tt = a.T > 148 * 8 ? std::max<int64_t>(1, kVecThreads / half) : 1;
-    tt = std::min<int64_t>(tt, 8);
+    int64_t tt = std::max<int64_t>(1, kVecThreads / half);
+    tt = std::min<int64_t>(tt, std::max<int64_t>(1, a.T / (148 * 8)));
     const int64_t grid = (a.T + tt - 1) / tt;
     if (grid <= INT32_MAX) {
       cfg.gridDim = dim3((unsigned)grid);

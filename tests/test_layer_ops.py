@@ -428,6 +428,32 @@ def test_append_bit_exact(L, H, D, page, bt, dtype):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", [bq.INT8, bq.FP8_E4M3])
+def test_append_codes_of_many_values_bit_exact(L, dtype):
+    """The cache write forms its quotients without divisions: every bf16 value
+    against scales of all magnitudes, and scales that lie next to a power of two."""
+    g = gen(23 + dtype)
+    H, D, page = 1, 128, 64
+    every = torch.arange(0, 0x7F80, device="cuda", dtype=torch.int32).to(torch.int16)
+    every = torch.cat([every, every | -0x8000]).view(torch.bfloat16)     # all finite values
+    for step in range(40):
+        e = 2.0 ** (step * 6 - 120)
+        top = (every.abs().float() <= e).nonzero()[:, 0]
+        # values near the block's largest, where codes are not all zero, in random order
+        near = top[every[top].abs().float() > e * 2.0 ** -14]
+        x = every[near[torch.randint(0, near.numel(), (64 * D * 4,), generator=g, device="cuda")]]
+        x = x.view(256, H, D)
+        i32 = dict(dtype=torch.int32, device="cuda")
+        off, lens = torch.tensor([0, 256], **i32), torch.tensor([256], **i32)
+        table = torch.arange(4, **i32).view(1, 4)
+        c = bq.kv_cache(4, H, page, D, page, dtype)
+        want = ref.append(c.k, c.ks, x, off, lens, table, dtype)
+        bq.kv_append(c, x, x, off, lens, table)
+        assert torch.equal(c.ks, want[1]) and torch.equal(c.k, want[0]), step
+        assert torch.equal(c.v, c.k)
+
+
+@gpu
 def test_append_skips_and_records_what_it_cannot_use(L):
     g = gen(5)
     i32 = dict(dtype=torch.int32, device="cuda")
