@@ -629,54 +629,68 @@ attn_tc_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles) {
       ok = wait_bar(&o_last[t], 0, abort_flag, a.status, 0x73Bu);
     if (ok && !idle) {
       tc_fence_after();
-      const int64_t tok = s.row0 + (row_on ? row / g : 0);
-      const int head = hk * g + (row_on ? row % g : 0);
+      // O goes out 32 columns at a time by way of this row tile's queries, which no
+      // product reads any more: a lane stores its row's 16-byte units, eight lanes
+      // then write one row's 128 bytes side by side.
       const bool whole = parts.splits == 1;
-      const int64_t pi = (tok * a.Hq + head) * parts.splits + split;
       const float f = whole ? (l == 0.f ? 0.f : __fdiv_rn(1.f, l)) : 1.f;
-      uint16_t* out = a.out + tok * a.ldo + (int64_t)head * a.ho;
-      const bool vec = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
+      const bool vec = ((reinterpret_cast<uintptr_t>(a.out) | (uintptr_t)(2 * a.ldo) |
+                         (uintptr_t)(2 * a.ho)) & 7) == 0;
+      const uint32_t stage = sbase + L::kQ + (uint32_t)t * L::kTile + (uint32_t)(warp & 3) * 4096u;
+      const int unit = lane & 7, first = R0 + 32 * warp + (lane >> 3);
+      int64_t at[8];                       // of rows first + 4 i, or -1
 #pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int rw = first + 4 * i;
+        const int64_t tok = s.row0 + rw / g, head = hk * g + rw % g;
+        at[i] = rw >= n_rows ? -1
+                : whole      ? tok * a.ldo + head * a.ho
+                             : ((tok * a.Hq + head) * parts.splits + split) * D;
+      }
+#pragma unroll 1
       for (int q = 0; q < D / 32; ++q) {
         uint32_t r[32];
         if (nt > 0) {
           tmem_ld32(ot + 32 * q, r);
           tmem_ld_wait();
         }
-        if (!row_on) continue;
-        if (!whole) {
-          if (l != 0.f) {
-            float4* o = reinterpret_cast<float4*>(parts.o + pi * D + 32 * q);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              o[e] = make_float4(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1]),
-                                 __uint_as_float(r[4 * e + 2]), __uint_as_float(r[4 * e + 3]));
+        for (int u = 0; u < 8; ++u) {
+          float x[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] = l == 0.f ? 0.f : __uint_as_float(r[4 * u + e]) * f;
+          st_shared16(stage + sw128(lane, u), __float_as_uint(x[0]), __float_as_uint(x[1]),
+                      __float_as_uint(x[2]), __float_as_uint(x[3]));
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float4 x = *reinterpret_cast<const float4*>(
+              smem + (stage - sbase) + sw128(4 * i + (lane >> 3), unit));
+          if (at[i] < 0) continue;
+          const int64_t d = at[i] + 32 * q + 4 * unit;
+          if (!whole) {
+            *reinterpret_cast<float4*>(parts.o + d) = x;
+          } else if (vec) {
+            uint2 w;
+            w.x = (uint32_t)float_to_bf16_bits(x.x) | (uint32_t)float_to_bf16_bits(x.y) << 16;
+            w.y = (uint32_t)float_to_bf16_bits(x.z) | (uint32_t)float_to_bf16_bits(x.w) << 16;
+            *reinterpret_cast<uint2*>(a.out + d) = w;
+          } else {
+            a.out[d] = float_to_bf16_bits(x.x);
+            a.out[d + 1] = float_to_bf16_bits(x.y);
+            a.out[d + 2] = float_to_bf16_bits(x.z);
+            a.out[d + 3] = float_to_bf16_bits(x.w);
           }
-          continue;
         }
-        uint32_t w[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float x0 = l == 0.f ? 0.f : __uint_as_float(r[2 * e]) * f;
-          const float x1 = l == 0.f ? 0.f : __uint_as_float(r[2 * e + 1]) * f;
-          w[e] = (uint32_t)float_to_bf16_bits(x0) | (uint32_t)float_to_bf16_bits(x1) << 16;
-        }
-        if (vec) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            *reinterpret_cast<uint4*>(out + 32 * q + 8 * e) =
-                make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            out[32 * q + 2 * e] = (uint16_t)w[e];
-            out[32 * q + 2 * e + 1] = (uint16_t)(w[e] >> 16);
-          }
-        }
+        __syncwarp();
       }
       if (row_on) {
+        const int64_t tok = s.row0 + row / g, head = hk * g + row % g;
         if (!whole)
-          *reinterpret_cast<float2*>(parts.stat + 2 * pi) = make_float2(l, mo);
+          *reinterpret_cast<float2*>(parts.stat +
+                                     2 * ((tok * a.Hq + head) * parts.splits + split)) =
+              make_float2(l, mo);
         else if (a.lse)
           a.lse[tok * a.Hq + head] =
               l == 0.f ? -INFINITY : (mo + log2f(l)) * 0.6931471805599453f;
@@ -743,13 +757,25 @@ int64_t attn_tc_tiles(int64_t max_q, int64_t group) {
 
 bool attn_tc_takes(int64_t D, int64_t page) { return (D == 64 || D == 128) && page % 16 == 0; }
 
-// One CTA runs on an SM: keys are split where there are fewer CTAs than SMs, in
-// parts of at least 512.
+// One CTA runs on an SM, so a call takes as many rounds of CTAs as units / 148,
+// rounded up; splitting the keys evens the rounds out.  In units of a key tile
+// (2.8 us measured): a CTA's start and end are about two, and the partial rows of a
+// split, 1 KB a row written and read, units * 256 KB at 6.5 TB/s.
 int attn_tc_chunk(int64_t B, int64_t Hkv, int64_t max_q, int64_t group, int64_t span) {
   const int64_t units = std::max<int64_t>(1, B * Hkv * attn_tc_tiles(max_q, group));
-  const int64_t parts = std::max<int64_t>(1, 148 / units);
-  if (parts == 1) return 1 << 30;
-  return (int)std::max<int64_t>(512, ((span + parts - 1) / parts + BN - 1) / BN * BN);
+  const int64_t tiles = std::max<int64_t>(1, (span + BN - 1) / BN);
+  int64_t best = 1;
+  double least = 0.0;
+  for (int64_t p = 1; p <= 64 && (p == 1 || tiles / p >= 4); ++p) {
+    const int64_t per = (tiles + p - 1) / p;
+    const double cost = (double)((units * p + 147) / 148) * (double)(per + 2) +
+                        (p > 1 ? 1.0 + 0.0144 * (double)(units * p) : 0.0);
+    if (p == 1 || cost < least) {
+      least = cost;
+      best = p;
+    }
+  }
+  return best == 1 ? 1 << 30 : (int)((tiles + best - 1) / best * BN);
 }
 
 cudaError_t launch_attn_tc(const AttnArgs& a, const AttnParts& p, cudaStream_t st) {

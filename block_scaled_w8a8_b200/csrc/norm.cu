@@ -42,19 +42,20 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
-// y of eight elements: r, w as packed bf16.
-__device__ __forceinline__ void normed(const uint4& r, const uint4& w, float rstd, float w_off,
-                                       float (&y)[8]) {
+// t = r (w + w_off) of eight elements, r and w as packed bf16: exact in fp32 for
+// w_off = 0.
+__device__ __forceinline__ void weighted(const uint4& r, const uint4& w, float w_off,
+                                         float (&t)[8]) {
   const uint32_t rr[4] = {r.x, r.y, r.z, r.w}, ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    y[2 * e] = __uint_as_float(rr[e] << 16) * rstd * (__uint_as_float(ww[e] << 16) + w_off);
-    y[2 * e + 1] = __uint_as_float(rr[e] & 0xFFFF0000u) * rstd *
+    t[2 * e] = __uint_as_float(rr[e] << 16) * (__uint_as_float(ww[e] << 16) + w_off);
+    t[2 * e + 1] = __uint_as_float(rr[e] & 0xFFFF0000u) *
                    (__uint_as_float(ww[e] & 0xFFFF0000u) + w_off);
   }
 }
 
-// Four codes of y * inv, |y * inv| <= 127 (1 + 2^-22).
+// Four codes of y * inv, |y * inv| <= 127 (1 + 2^-22): round to nearest even.
 __device__ __forceinline__ uint32_t int8x4(const float* y, float inv) {
   uint32_t b[4];
 #pragma unroll
@@ -101,8 +102,8 @@ __global__ void __launch_bounds__(kAnyThreads) norm_any_kernel(const NormArgs a)
       const int64_t k0 = g * a.group, k1 = min(k0 + a.group, a.K);
       float amax = 0.f;
       for (int64_t k = k0 + lane; k < k1; k += 32)
-        amax = fmaxf(amax, fabsf(bf16_bits_to_float(row[k]) * rstd *
-                                 (bf16_bits_to_float(a.w[k]) + a.w_off)));
+        amax = fmaxf(amax, fabsf(bf16_bits_to_float(row[k]) *
+                                 (bf16_bits_to_float(a.w[k]) + a.w_off) * rstd));
       amax = warp_max(amax);
       float sc = 0.f, inv = 0.f;
       if (DT == kMxFp8) {
@@ -114,8 +115,8 @@ __global__ void __launch_bounds__(kAnyThreads) norm_any_kernel(const NormArgs a)
         if (lane == 0) a.s[g * a.M + m] = sc;
       }
       for (int64_t k = k0 + lane; k < k1; k += 32) {
-        const float y = bf16_bits_to_float(row[k]) * rstd *
-                        (bf16_bits_to_float(a.w[k]) + a.w_off);
+        const float y = bf16_bits_to_float(row[k]) *
+                        (bf16_bits_to_float(a.w[k]) + a.w_off) * rstd;
         if (DT == kMxFp8)
           a.q[m * a.ldq + k] = (uint8_t)(e4m3x2_code(y * inv, 0.f, 1.0f) & 0xFFu);
         else
@@ -131,13 +132,13 @@ __global__ void __launch_bounds__(kAnyThreads) norm_any_kernel(const NormArgs a)
 // the whole row): a CTA per row, V vectors of 8 elements a thread, everything in
 // registers, one barrier a row.  Memory-bound: x and the residual are read once,
 // the sum, the codes and the scales written once; the next row is under way while
-// one is reduced.  In place is safe: a row is loaded and stored by one CTA, each
+// one is reduced (up to 16384 columns).  In place is safe: a row is loaded and stored by one CTA, each
 // element by one thread, loads first.
 //
-// Codes are formed with the reciprocal of the scale: y itself is only good to an
-// fp32 rounding, and one more of those moves a code only where y / s lies within
-// that of a border.  INT8: fma(y, 1/s, 1.5 * 2^23) rounds to nearest even and
-// leaves the code in the low byte, with no conversion unit involved.
+// y = t rstd with t = r (w + w_off), and rstd falls out of y / s: the codes are those
+// of t Q / max |t|, where only Q / max |t| and the product round, and the scale is
+// max |t| rstd / Q.  INT8: fma(t, Q / max |t|, 1.5 * 2^23) rounds to nearest even
+// and leaves the code in the low byte, with no conversion unit involved.
 template <int DT, int V>
 __global__ void __launch_bounds__(V <= 2 ? 1024 : 512)
 norm_vec_kernel(const NormArgs a, const int lpg) {       // lpg: lanes of a group, 0 = the row
@@ -167,16 +168,18 @@ norm_vec_kernel(const NormArgs a, const int lpg) {       // lpg: lanes of a grou
       }
     }
   };
-  if (blockIdx.x < a.M) load(blockIdx.x);
+  constexpr bool kAhead = V <= 2;           // wider rows have no registers for it
+  if (kAhead && blockIdx.x < a.M) load(blockIdx.x);
   int parity = 0;
   for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x, parity ^= 1) {
     uint4 rv[V], sv[V];
+    if (!kAhead) load(m);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       rv[i] = nx[i];
       sv[i] = ns[i];
     }
-    if (m + gridDim.x < a.M) load(m + gridDim.x);
+    if (kAhead && m + gridDim.x < a.M) load(m + gridDim.x);
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -205,10 +208,10 @@ norm_vec_kernel(const NormArgs a, const int lpg) {       // lpg: lanes of a grou
     if (lpg == 0) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        float y[8];
-        normed(rv[i], wv[i], rstd, a.w_off, y);
+        float t[8];
+        weighted(rv[i], wv[i], a.w_off, t);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) row_max = fmaxf(row_max, fabsf(y[e]));
+        for (int e = 0; e < 8; ++e) row_max = fmaxf(row_max, fabsf(t[e]));
       }
       row_max = warp_max(row_max);
       if (lane == 0) red[parity][1][warp] = row_max;
@@ -218,11 +221,11 @@ norm_vec_kernel(const NormArgs a, const int lpg) {       // lpg: lanes of a grou
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int v = i * nt + tid;
-      float y[8];
-      normed(rv[i], wv[i], rstd, a.w_off, y);
-      float amax = 0.f;
+      float t[8];
+      weighted(rv[i], wv[i], a.w_off, t);
+      float amax = 0.f;                        // of t
 #pragma unroll
-      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(y[e]));
+      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(t[e]));
 #pragma unroll
       for (int o = 16; o >= 1; o >>= 1)
         if (o < lpg) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
@@ -232,18 +235,24 @@ norm_vec_kernel(const NormArgs a, const int lpg) {       // lpg: lanes of a grou
       const int64_t g = lpg == 0 ? 0 : v / lpg;
       uint2 q;
       if (DT == kMxFp8) {
-        const int se = mx_exponent(amax);
+        const int se = mx_exponent(amax * rstd);
         const float inv = __uint_as_float((uint32_t)(127 - se) << 23);   // 2^-se, exact
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = t[e] * rstd;
         q.x = e4m3x4(y, inv);
         q.y = e4m3x4(y + 4, inv);
         if (first) a.sf[mx_sf_index(m, g, a.K)] = (uint8_t)(se + 127);
       } else {
-        const float sc = group_scale<DT>(amax);
-        if (sc >= 0x1p-100f) {
-          const float inv = __fdiv_rn(1.0f, sc);
-          q.x = DT == kInt8 ? int8x4(y, inv) : e4m3x4(y, inv);
-          q.y = DT == kInt8 ? int8x4(y + 4, inv) : e4m3x4(y + 4, inv);
-        } else {                               // the reciprocal may not be a number
+        const float sc = group_scale<DT>(amax * rstd);
+        if (amax >= 0x1p-100f && amax <= 0x1p100f) {
+          const float f = __fdiv_rn(DT == kInt8 ? 127.0f : 448.0f, amax);
+          q.x = DT == kInt8 ? int8x4(t, f) : e4m3x4(t, f);
+          q.y = DT == kInt8 ? int8x4(t + 4, f) : e4m3x4(t + 4, f);
+        } else {                               // the factor may not be a number
+          float y[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = t[e] * rstd;
           q.x = pack4_codes<DT == kMxFp8 ? kFp8 : DT>(y, sc);
           q.y = pack4_codes<DT == kMxFp8 ? kFp8 : DT>(y + 4, sc);
         }
@@ -252,8 +261,8 @@ norm_vec_kernel(const NormArgs a, const int lpg) {       // lpg: lanes of a grou
       *reinterpret_cast<uint2*>(a.q + m * a.ldq + 8 * (int64_t)v) = q;
       if (a.h)
         reinterpret_cast<uint4*>(a.h + m * a.ldh)[v] =
-            make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]),
-                       pack_bf16(y[6], y[7]));
+            make_uint4(pack_bf16(t[0] * rstd, t[1] * rstd), pack_bf16(t[2] * rstd, t[3] * rstd),
+                       pack_bf16(t[4] * rstd, t[5] * rstd), pack_bf16(t[6] * rstd, t[7] * rstd));
     }
   }
 }
