@@ -196,10 +196,12 @@ __device__ __forceinline__ void fence_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// UNI: block_t is a multiple of 16, so that 16 aligned tokens share their scales;
-// the scales of a tile are then eight entries {cs, lg2 vs, 1 / vs, -} and the
-// weights cost half the instructions (prompt of 8192, block_t 64: see launch_dt).
-template <int DT, int D, bool UNI>
+// UNI: aligned tokens that share their scales: 64 (a score block), 16 or 0, as
+// block_t is a multiple of them.  With 16 the scales of a tile are eight entries
+// {cs, lg2 vs, 1 / vs, -}, with 64 a score block has one of them.  Prompt of 8192,
+// block_t 64: 912, 688, 645 us with 0, 16, 64; three chunks of 513 over 6000 keys,
+// block_t 16: 226, 173 us with 0, 16.
+template <int DT, int D, int UNI>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_tc_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles) {
   using L = Lay<D>;
@@ -520,6 +522,10 @@ attn_tc_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles) {
           reinterpret_cast<const float4*>(smem + L::kSc + (uint32_t)(j & 3) * L::kScSlot) +
           (UNI ? 4 : SN / 4) * (i & 1);
       const bool masked = t0 < in_lo || t0 + SN > in_hi;
+      float4 one;                          // UNI == SN: the block's scales
+      if constexpr (UNI == SN) {
+        group_scales(sc4 + (t0 < all.lo ? min(3, (all.lo - t0) >> 4) : 0), rd, one.x, one.y, one.z);
+      }
       const int a0 = row_lo - t0, a1 = row_hi - t0;
       // all scores at once: a load's latency is near that of a whole row
       uint32_t y[SN];
@@ -553,7 +559,7 @@ attn_tc_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles) {
           m1 = max3(__float_as_uint(m1), y[16 * q + i + 2], y[16 * q + i + 3]);
         }
         m0 = max3(__float_as_uint(m0), y[16 * q + 14], y[16 * q + 15]);
-        if constexpr (UNI) {
+        if constexpr (UNI == 16) {
           float c, lv, iv;
           group_scales(sc4 + q, rd, c, lv, iv);
           mx = fmaxf(mx, fmaf(c, fmaxf(m0, m1), lv));
@@ -561,6 +567,7 @@ attn_tc_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles) {
           mx = max3(__float_as_uint(mx), __float_as_uint(m0), __float_as_uint(m1));
         }
       }
+      if constexpr (UNI == SN) mx = fmaf(one.x, mx, one.y);
       const bool up = mx > mo + kLazy || (mo == -INFINITY && mx != -INFINITY);
       if (__any_sync(0xffffffffu, up)) {
         const float f = up ? ex2(mo - mx) : 1.f;     // 0 for the first keys seen
@@ -584,6 +591,7 @@ attn_tc_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles) {
         }
       }
       const float neg = -finite(mo);
+      uint64_t sums[2] = {0, 0};
 #pragma unroll
       for (int h = 0; h < SN / 32; ++h) {
         uint32_t p[16];
@@ -592,9 +600,16 @@ attn_tc_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles) {
           const uint32_t* w = y + 32 * h + 16 * u;
           if constexpr (UNI) {
             float c, lv, iv;
-            group_scales(sc4 + 2 * h + u, rd, c, lv, iv);
+            if constexpr (UNI == SN) {
+              c = one.x;
+              lv = one.y;
+              iv = one.z;
+            } else {
+              group_scales(sc4 + 2 * h + u, rd, c, lv, iv);
+            }
             const uint64_t c2 = pack2(c, c), b2 = pack2(lv + neg, lv + neg);
-            uint64_t sum = 0;
+            uint64_t& sum = sums[u];
+            if (UNI != SN) sum = 0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const uint64_t d = fma2((uint64_t)w[2 * i + 1] << 32 | w[2 * i], c2, b2);
@@ -602,7 +617,7 @@ attn_tc_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles) {
               sum = add2(sum, pack2(p0, p1));
               p[8 * u + i] = pack_f16(p0, p1);
             }
-            l = fmaf(lo2(sum) + hi2(sum), iv, l);
+            if (UNI != SN) l = fmaf(lo2(sum) + hi2(sum), iv, l);
           } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -623,6 +638,10 @@ attn_tc_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles) {
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
+      if constexpr (UNI == SN) {
+        const uint64_t sum = add2(sums[0], sums[1]);
+        l = fmaf(lo2(sum) + hi2(sum), one.z, l);
+      }
       if (lane == 0) mbar_arrive(smem_u32(&p_ready[2 * t + (i & 1)]));
     }
     if (nt > 0 && !idle && ok)
@@ -705,7 +724,7 @@ attn_tc_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles) {
   }
 }
 
-template <int DT, int D, bool UNI>
+template <int DT, int D, int UNI>
 cudaError_t launch_t(const AttnArgs& a, const AttnParts& p, cudaStream_t st) {
   auto kern = attn_tc_kernel<DT, D, UNI>;
   static bool ready[64] = {};
@@ -743,10 +762,14 @@ cudaError_t launch_t(const AttnArgs& a, const AttnParts& p, cudaStream_t st) {
 
 template <int DT>
 cudaError_t launch_dt(const AttnArgs& a, const AttnParts& p, cudaStream_t st) {
-  const bool uni = a.c.bt % 16 == 0;
+  const int uni = a.c.bt % SN == 0 ? SN : a.c.bt % 16 == 0 ? 16 : 0;
   if (a.c.D == 64)
-    return uni ? launch_t<DT, 64, true>(a, p, st) : launch_t<DT, 64, false>(a, p, st);
-  return uni ? launch_t<DT, 128, true>(a, p, st) : launch_t<DT, 128, false>(a, p, st);
+    return uni == SN ? launch_t<DT, 64, SN>(a, p, st)
+           : uni     ? launch_t<DT, 64, 16>(a, p, st)
+                     : launch_t<DT, 64, 0>(a, p, st);
+  return uni == SN ? launch_t<DT, 128, SN>(a, p, st)
+         : uni     ? launch_t<DT, 128, 16>(a, p, st)
+                   : launch_t<DT, 128, 0>(a, p, st);
 }
 
 }  // namespace
@@ -759,7 +782,7 @@ bool attn_tc_takes(int64_t D, int64_t page) { return (D == 64 || D == 128) && pa
 
 // One CTA runs on an SM, so a call takes as many rounds of CTAs as units / 148,
 // rounded up; splitting the keys evens the rounds out.  In units of a key tile
-// (2.8 us measured): a CTA's start and end are about two, and the partial rows of a
+// (2.7 us measured): a CTA's start and end are about two, and the partial rows of a
 // split, 1 KB a row written and read, units * 256 KB at 6.5 TB/s.
 int attn_tc_chunk(int64_t B, int64_t Hkv, int64_t max_q, int64_t group, int64_t span) {
   const int64_t units = std::max<int64_t>(1, B * Hkv * attn_tc_tiles(max_q, group));
