@@ -180,9 +180,11 @@ cudaError_t launch_pdl(void (*kernel)(Args...), int64_t grid, int threads, cudaS
 // The kernel of a call and how it splits the keys, from the call's sizes alone.
 enum class Path { kAny, kDecode, kTc };
 
-// Up to 32 rows per key head the decode kernel streams the codes at most twice;
-// beyond that the tensor cores win.
-constexpr int64_t kDecodeRows = 32;
+// Rows per key head up to which the streaming kernel is taken; it reads the codes
+// once for 8 rows, the tensor core kernel once for 256 but with a dearer start.  16
+// sequences of 8192 keys: 16 rows 121 and 163 us, 24 rows 156 and 163; 1 of 65536:
+// 16 rows 75 and 88, 24 rows 94 and 88; 1 of 4096: 24 rows 17 and 22 us.
+constexpr int64_t kDecodeRows = 24;
 
 Path plan_path(int64_t D, int64_t page, int64_t rows) {
   if (rows > kDecodeRows && attn_tc_takes(D, page)) return Path::kTc;

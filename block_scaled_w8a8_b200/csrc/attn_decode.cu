@@ -1,8 +1,8 @@
 // attn_decode.cu -- attention over the paged 8-bit cache for few query rows
 // per key head (decoding): bound by the stream of codes from memory.
 //
-// A CTA works on up to 8 NR rows (tokens x heads of one key head's group) and
-// one part of the keys; its four warps take groups of 16 NG tokens in turn.
+// A CTA works on 8 rows (tokens x heads of one key head's group) and one part
+// of the keys; its four warps take groups of 16 NG tokens in turn.
 // Codes go from global memory straight into the registers that the matrix
 // instruction wants, with no pass through shared memory:
 //   S^T = K Q^T   A = 16 tokens x 16 dims.  Which dims a k-step takes is free
@@ -13,6 +13,9 @@
 //                 dims from r D / 8 on, of tokens 2c, 2c+1, 2c+8, 2c+9 (8 lanes =
 //                 one row of D bytes); a byte permute pairs two tokens' codes.
 //                 P^T is S^T's accumulator, transposed in registers (movmatrix).
+// More rows are more row tiles, side by side in the grid, whose codes come from L2:
+// 16 x 8192 keys, 8 rows 78 us, 16 rows 120 us (two row tiles in one CTA, whose
+// registers leave room for half as many warps: 134 us).
 // A group's registers take the next group's codes as soon as the product that
 // reads them has been issued, so a warp has about 4 KB under way and needs no
 // second set of registers.
@@ -42,10 +45,10 @@ namespace {
 
 using namespace attn;
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 4, R = 8;        // R: rows of a CTA
 
 // One group of 16 tokens as it comes from memory.
-template <int D, bool UNI>
+template <int D, int UNI>
 struct Group {
   uint4 k[2][D / 64];           // tokens r, r + 8
   uint32_t v[4][D / 32];        // tokens 2c, 2c + 1, 2c + 8, 2c + 9: D / 8 bytes each
@@ -58,36 +61,40 @@ struct Place {
   int idx, slot;
 };
 
-// UNI: block_t is a multiple of 16, so that the group shares its scales.
-template <int DT, int D, int NR, bool UNI>
-__global__ void __launch_bounds__(kWarps * 32, NR == 1 ? 4 : 2)
+// UNI: what of the tokens shares its scales and its page: 16 a group (block_t a
+// multiple of 16), 32 a step of two groups (D = 64, block_t a multiple of 32), 0
+// nothing.  2 x up to 131071 keys of dim 64, block_t 32: 68, 64, 56 us with 0, 16,
+// 32; 64 x up to 8192 keys of dim 128, block_t 64: 143, 138 us with 0, 16.
+template <int DT, int D, int UNI>
+__global__ void __launch_bounds__(kWarps * 32, 4)
 attn_decode_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles) {
   constexpr int NG = 128 / D;              // groups of 16 tokens in flight: 4 KB of codes a warp
   constexpr int KS = D / 16;               // k-steps of the score product
-  constexpr int R = 8 * NR;
   constexpr int SC = UNI ? 1 : 2;
+  constexpr int NP = UNI == 32 ? NG / 2 : NG, TP = 16 * NG / NP;   // places of a step, their tokens
   __shared__ float so[kWarps][R][D + 4];
   __shared__ float st[kWarps][R][2];
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
-  const int split = (int)(blockIdx.x % (unsigned)parts.splits);
-  const int bt_ = (int)(blockIdx.x / (unsigned)parts.splits);
-  const int rt = bt_ % row_tiles, b = bt_ / row_tiles, hk = blockIdx.y;
+  // row tiles of the same keys side by side: the second one's codes come from L2
+  const int rt = (int)(blockIdx.x % (unsigned)row_tiles);
+  const int bs = (int)(blockIdx.x / (unsigned)row_tiles);
+  const int split = bs % parts.splits, b = bs / parts.splits, hk = blockIdx.y;
   const int g = a.Hq / a.c.H, page = a.c.page;
   const int32_t* table = a.b.table + (int64_t)b * a.b.ld_table;
   constexpr int STEP = 16 * NG, STRIDE = kWarps * STEP;
   // without a window a split begins at a place known beforehand: its first pages
   // are asked for together with the sequence's length
-  Place at[2][NG];                         // of the next two rounds' groups
-  int32_t pg[2][NG];                       // their pages
+  Place at[2][NP];                         // of the next two rounds' groups
+  int32_t pg[2][NP];                       // their pages
   auto pages = [&](int t, int end) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int u = 0; u < NG; ++u) {
-        const int64_t tu = (int64_t)t + h * STRIDE + 16 * u;
+      for (int u = 0; u < NP; ++u) {
+        const int64_t tu = (int64_t)t + h * STRIDE + TP * u;
         const int idx = (int)(tu / page);
         at[h][u] = {idx, (int)(tu - (int64_t)idx * page)};
         pg[h][u] = tu < end ? table[idx] : -1;
@@ -126,15 +133,16 @@ attn_decode_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles)
     return -1;
   };
   Group<D, UNI> G[NG];
-  bool ok[NG];                             // the group's page exists (warp-uniform)
+  bool ok[NP];                             // the group's page exists (warp-uniform)
   auto load_k = [&](int u, int64_t ph) {
-    const int slot = at[0][u].slot;
+    const int slot = at[0][u * NP / NG].slot + (16 * u) % TP;
     if (ph < 0) return;
     const uint8_t* p = kbase + (ph * page + slot) * D;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int i = 0; i < D / 64; ++i) G[u].k[h][i] = ld_codes16(p + h * 8 * D + 64 * i);
+    if ((16 * u) % TP) return;             // the place's scales are there already
 #pragma unroll
     for (int h = 0; h < SC; ++h) {
       const unsigned x = (unsigned)(slot + (UNI ? 0 : r + 8 * h));
@@ -142,93 +150,87 @@ attn_decode_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles)
     }
   };
   auto load_v = [&](int u, int64_t ph) {
-    const int slot = at[0][u].slot;
+    const int slot = at[0][u * NP / NG].slot + (16 * u) % TP;
     if (ph < 0) return;
     const uint8_t* p = vbase + (ph * page + slot) * D;
 #pragma unroll
     for (int e = 0; e < 4; ++e) ld_codes<D>(p + ((e & 1) + 8 * (e >> 1)) * D, G[u].v[e]);
+    if ((16 * u) % TP) return;
 #pragma unroll
     for (int h = 0; h < SC; ++h) {
       const unsigned x = (unsigned)(slot + (UNI ? 0 : r + 8 * h));
       G[u].vs[h] = a.c.vs[ph * nblk + (bt > 1 ? __umulhi(x, bt_inv) : x)];
     }
   };
-  int64_t ph[NG];
+  int64_t ph[NP];
+#pragma unroll
+  for (int u = 0; u < NP; ++u) {
+    ph[u] = row_of(u, t + TP * u);
+    ok[u] = ph[u] >= 0;
+  }
 #pragma unroll
   for (int u = 0; u < NG; ++u) {
-    ph[u] = row_of(u, t + 16 * u);
-    ok[u] = ph[u] >= 0;
-    load_k(u, ph[u]);
-    load_v(u, ph[u]);
+    load_k(u, ph[u * NP / NG]);
+    load_v(u, ph[u * NP / NG]);
   }
 
-  // queries: row R0 + 8 nt + r of lane (r, c), dims 64 i + 16 c .. + 15
-  uint32_t qf[NR][KS][2];
-  float rowfac[NR][2];
-  int row_lo[NR][2], row_hi[NR][2];        // of the rows 2c, 2c + 1 whose scores this lane gets
+  // queries: row R0 + r of lane (r, c), dims 64 i + 16 c .. + 15
+  uint32_t qf[KS][2];
+  float rowfac[2];
+  const int row = R0 + r;
+  const bool on = row < n_rows;
+  const uint16_t* q = a.q + (int64_t)(s.row0 + (on ? row / g : 0)) * a.ldq +
+                      (int64_t)(hk * g + (on ? row % g : 0)) * a.hq;
+  uint32_t w[KS][2];                     // bf16 pairs: word 2 (k-step) + e of the row's part
+  const bool vec = (reinterpret_cast<uintptr_t>(q) & 15) == 0;
 #pragma unroll
-  for (int nt = 0; nt < NR; ++nt) {
-    const int row = R0 + 8 * nt + r;
-    const bool on = row < n_rows;
-    const uint16_t* q = a.q + (int64_t)(s.row0 + (on ? row / g : 0)) * a.ldq +
-                        (int64_t)(hk * g + (on ? row % g : 0)) * a.hq;
-    uint32_t w[KS][2];                     // bf16 pairs: word 2 (k-step) + e of the row's part
-    const bool vec = (reinterpret_cast<uintptr_t>(q) & 15) == 0;
+  for (int ks = 0; ks < KS; ks += 2) {
+    const uint16_t* p = q + 64 * (ks >> 2) + 16 * c + 4 * (ks & 3);
+    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+    if (on && vec) x = *reinterpret_cast<const uint4*>(p);
+    else if (on)
+      x = make_uint4(p[0] | (uint32_t)p[1] << 16, p[2] | (uint32_t)p[3] << 16,
+                     p[4] | (uint32_t)p[5] << 16, p[6] | (uint32_t)p[7] << 16);
+    w[ks][0] = x.x; w[ks][1] = x.y; w[ks + 1][0] = x.z; w[ks + 1][1] = x.w;
+  }
+  float amax = 0.f;
 #pragma unroll
-    for (int ks = 0; ks < KS; ks += 2) {
-      const uint16_t* p = q + 64 * (ks >> 2) + 16 * c + 4 * (ks & 3);
-      uint4 x = make_uint4(0u, 0u, 0u, 0u);
-      if (on && vec) x = *reinterpret_cast<const uint4*>(p);
-      else if (on)
-        x = make_uint4(p[0] | (uint32_t)p[1] << 16, p[2] | (uint32_t)p[3] << 16,
-                       p[4] | (uint32_t)p[5] << 16, p[6] | (uint32_t)p[7] << 16);
-      w[ks][0] = x.x; w[ks][1] = x.y; w[ks + 1][0] = x.z; w[ks + 1][1] = x.w;
-    }
-    float amax = 0.f;
+  for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks)
+    for (int e = 0; e < 2; ++e)
+      amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[ks][e] << 16)),
+                               fabsf(__uint_as_float(w[ks][e] & 0xFFFF0000u))));
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+  float up, down;
+  row_power(amax, up, down);
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-        amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[ks][e] << 16)),
-                                 fabsf(__uint_as_float(w[ks][e] & 0xFFFF0000u))));
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    float up, down;
-    row_power(amax, up, down);
+  for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks)
+    for (int e = 0; e < 2; ++e)
+      qf[ks][e] = pack_f16(__uint_as_float(w[ks][e] << 16) * up,
+                               __uint_as_float(w[ks][e] & 0xFFFF0000u) * up);
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-        qf[nt][ks][e] = pack_f16(__uint_as_float(w[ks][e] << 16) * up,
-                                 __uint_as_float(w[ks][e] & 0xFFFF0000u) * up);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      rowfac[nt][j] = __shfl_sync(0xffffffffu, down, 4 * (2 * c + j)) * (a.scale * kLog2e);
-      // rows behind the last stand in for it (their queries are zero, nothing is written)
-      const int i = min((R0 + 8 * nt + 2 * c + j) / g, s.n - 1);
-      row_range(a, s, i, row_lo[nt][j], row_hi[nt][j]);
-    }
+  for (int j = 0; j < 2; ++j) {
+    rowfac[j] = __shfl_sync(0xffffffffu, down, 4 * (2 * c + j)) * (a.scale * kLog2e);
   }
   // every row of the tile sees the tokens of [in_lo, in_hi)
   int unused, in_lo, in_hi;
   row_range(a, s, i_hi, in_lo, unused);
   row_range(a, s, i_lo, unused, in_hi);
 
-  float o[NR][KS][4], l[NR][2], mo[NR][2];
+  float o[KS][4], l[2], mo[2];
 #pragma unroll
-  for (int nt = 0; nt < NR; ++nt) {
+  for (int i = 0; i < KS; ++i)
 #pragma unroll
-    for (int i = 0; i < KS; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
-    mo[nt][0] = mo[nt][1] = -INFINITY;
-    l[nt][0] = l[nt][1] = 0.f;
-  }
+    for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+  mo[0] = mo[1] = -INFINITY;
+  l[0] = l[1] = 0.f;
 
   for (; t < part.hi; t += STRIDE) {
     // the next round's pages are here; those of the one after it are asked for
 #pragma unroll
-    for (int u = 0; u < NG; ++u) {
+    for (int u = 0; u < NP; ++u) {
       at[0][u] = at[1][u];
       pg[0][u] = pg[1][u];
       at[1][u].idx += stride_idx;
@@ -237,121 +239,120 @@ attn_decode_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles)
         at[1][u].slot -= page;
         ++at[1][u].idx;
       }
-      pg[1][u] = (int64_t)t + 2 * STRIDE + 16 * u < part.hi ? table[at[1][u].idx] : -1;
+      pg[1][u] = (int64_t)t + 2 * STRIDE + TP * u < part.hi ? table[at[1][u].idx] : -1;
     }
     bool whole = t >= in_lo && t + STEP <= in_hi;
 #pragma unroll
-    for (int u = 0; u < NG; ++u) whole = whole && ok[u];
+    for (int u = 0; u < NP; ++u) whole = whole && ok[u];
     // scores, then y: e = 0, 1 rows 2c, 2c + 1 of token r; e = 2, 3 of token r + 8
-    float y[NR][NG][4];
+    float y[NG][4];
 #pragma unroll
     for (int u = 0; u < NG; ++u) {
 #pragma unroll
-      for (int nt = 0; nt < NR; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) y[nt][u][e] = 0.f;
+      for (int e = 0; e < 4; ++e) y[u][e] = 0.f;
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
         uint32_t f[4];
         codes_to_f16<DT>(word_of(G[u].k[0][ks >> 2], ks & 3), f[0], f[2]);
         codes_to_f16<DT>(word_of(G[u].k[1][ks >> 2], ks & 3), f[1], f[3]);
-#pragma unroll
-        for (int nt = 0; nt < NR; ++nt) mma_f16(y[nt][u], f, qf[nt][ks]);
+        mma_f16(y[u], f, qf[ks]);
       }
     }
-    float iv[NG][SC];
+    float iv[NP][SC], lv[NP][SC];
 #pragma unroll
-    for (int u = 0; u < NG; ++u) {
-      float lv[SC];
+    for (int u = 0; u < NP; ++u)
 #pragma unroll
       for (int h = 0; h < SC; ++h) {
-        const float vs = ok[u] ? fmaxf(G[u].vs[h], kMinVs) : 1.f;
-        lv[h] = lg2(vs);
+        const float vs = ok[u] ? fmaxf(G[u * NG / NP].vs[h], kMinVs) : 1.f;
+        lv[u][h] = lg2(vs);
         iv[u][h] = rcp(vs);
       }
 #pragma unroll
-      for (int nt = 0; nt < NR; ++nt)
+    for (int u = 0; u < NG; ++u) {
+      const int w = u * NP / NG;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          y[nt][u][e] = fmaf(y[nt][u][e], G[u].ks[UNI ? 0 : e >> 1] * rowfac[nt][e & 1],
-                             lv[UNI ? 0 : e >> 1]);
+      for (int e = 0; e < 4; ++e)
+        y[u][e] = fmaf(y[u][e], G[w * NG / NP].ks[UNI ? 0 : e >> 1] * rowfac[e & 1],
+                           lv[w][UNI ? 0 : e >> 1]);
     }
     // keys of the group after next are under way from here on
-    int64_t ph_next[NG];
+    int64_t ph_next[NP];
 #pragma unroll
-    for (int u = 0; u < NG; ++u) {
-      ph_next[u] = row_of(u, t + STRIDE + 16 * u);
-      load_k(u, ph_next[u]);
-    }
+    for (int u = 0; u < NP; ++u) ph_next[u] = row_of(u, t + STRIDE + TP * u);
+#pragma unroll
+    for (int u = 0; u < NG; ++u) load_k(u, ph_next[u * NP / NG]);
     if (!whole) {
 #pragma unroll
-      for (int u = 0; u < NG; ++u)
-#pragma unroll
-        for (int nt = 0; nt < NR; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int tok = t + 16 * u + r + 8 * (e >> 1), j = e & 1;
-            if (!ok[u] || tok < row_lo[nt][j] || tok >= row_hi[nt][j]) y[nt][u][e] = -INFINITY;
-          }
-    }
-    // weights
-    uint32_t pf[NR][NG][2];
-#pragma unroll
-    for (int nt = 0; nt < NR; ++nt) {
-      bool far = false;
-#pragma unroll
       for (int j = 0; j < 2; ++j) {
-        float mx = y[nt][0][j];
+        // the range of row 2c + j, whose scores this lane has; rows behind the last
+        // stand in for it (their queries are zero, nothing is written)
+        int lo, hi;
+        row_range(a, s, min((R0 + 2 * c + j) / g, s.n - 1), lo, hi);
 #pragma unroll
         for (int u = 0; u < NG; ++u)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) mx = fmaxf(mx, y[nt][u][2 * h + j]);
-        // the first keys of a row, or one far above its reference
-        far = far || mx > mo[nt][j] + 10.f;
-      }
-      if (__any_sync(0xffffffffu, far)) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float mx = mo[nt][j];
-#pragma unroll
-          for (int u = 0; u < NG; ++u)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) mx = fmaxf(mx, y[nt][u][2 * h + j]);
-#pragma unroll
-          for (int sh = 4; sh <= 16; sh <<= 1)
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
-          const float keep = ex2(mo[nt][j] - finite(mx));
-          l[nt][j] *= keep;
-          mo[nt][j] = mx;
-#pragma unroll
-          for (int i = 0; i < KS; ++i) {
-            o[nt][i][j] *= keep;
-            o[nt][i][2 + j] *= keep;
+          for (int h = 0; h < 2; ++h) {
+            const int tok = t + 16 * u + r + 8 * h;
+            if (!ok[u * NP / NG] || tok < lo || tok >= hi) y[u][2 * h + j] = -INFINITY;
           }
+      }
+    }
+    // weights
+    uint32_t pf[NG][2];
+    bool far = false;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float mx = y[0][j];
+#pragma unroll
+      for (int u = 0; u < NG; ++u)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) mx = fmaxf(mx, y[u][2 * h + j]);
+      // the first keys of a row, or one far above its reference
+      far = far || mx > mo[j] + 10.f;
+    }
+    if (__any_sync(0xffffffffu, far)) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float mx = mo[j];
+#pragma unroll
+        for (int u = 0; u < NG; ++u)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) mx = fmaxf(mx, y[u][2 * h + j]);
+#pragma unroll
+        for (int sh = 4; sh <= 16; sh <<= 1)
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
+        const float keep = ex2(mo[j] - finite(mx));
+        l[j] *= keep;
+        mo[j] = mx;
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+          o[i][j] *= keep;
+          o[i][2 + j] *= keep;
         }
       }
-      const float ref[2] = {finite(mo[nt][0]), finite(mo[nt][1])};
+    }
+    const float ref[2] = {finite(mo[0]), finite(mo[1])};
 #pragma unroll
-      for (int u = 0; u < NG; ++u) {
-        float p[4];
+    for (int u = 0; u < NG; ++u) {
+      float p[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) p[e] = ex2(y[nt][u][e] - ref[e & 1]);
+      for (int e = 0; e < 4; ++e) p[e] = ex2(y[u][e] - ref[e & 1]);
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          l[nt][j] = UNI ? fmaf(p[j] + p[2 + j], iv[u][0], l[nt][j])
-                         : fmaf(p[j], iv[u][0], fmaf(p[2 + j], iv[u][SC - 1], l[nt][j]));
-        pf[nt][u][0] = transpose8(pack_f16(p[0], p[1]));
-        pf[nt][u][1] = transpose8(pack_f16(p[2], p[3]));
-      }
+      for (int j = 0; j < 2; ++j)
+        l[j] = UNI ? fmaf(p[j] + p[2 + j], iv[u * NP / NG][0], l[j])
+                       : fmaf(p[j], iv[u * NP / NG][0],
+                              fmaf(p[2 + j], iv[u * NP / NG][SC - 1], l[j]));
+      pf[u][0] = transpose8(pack_f16(p[0], p[1]));
+      pf[u][1] = transpose8(pack_f16(p[2], p[3]));
     }
     // values
 #pragma unroll
     for (int u = 0; u < NG; ++u) {
-      if (!ok[u] || t + 16 * u < all.lo || t + 16 * u + 16 > part.hi) {
+      if (!ok[u * NP / NG] || t + 16 * u < all.lo || t + 16 * u + 16 > part.hi) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int tok = t + 16 * u + 2 * c + (e & 1) + 8 * (e >> 1);
-          const bool on = ok[u] && tok >= all.lo && tok < part.hi;
+          const bool on = ok[u * NP / NG] && tok >= all.lo && tok < part.hi;
 #pragma unroll
           for (int w = 0; w < D / 32; ++w) G[u].v[e][w] = on ? G[u].v[e][w] : 0u;
         }
@@ -365,35 +366,30 @@ attn_decode_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles)
           codes_to_f16<DT>(__byte_perm(x, z, 0x5140), f0[2 * h], f0[2 * h + 1]);
           codes_to_f16<DT>(__byte_perm(x, z, 0x7362), f1[2 * h], f1[2 * h + 1]);
         }
-#pragma unroll
-        for (int nt = 0; nt < NR; ++nt) {
-          mma_f16(o[nt][2 * w], f0, pf[nt][u]);
-          mma_f16(o[nt][2 * w + 1], f1, pf[nt][u]);
-        }
+        mma_f16(o[2 * w], f0, pf[u]);
+        mma_f16(o[2 * w + 1], f1, pf[u]);
       }
-      load_v(u, ph_next[u]);
-      ok[u] = ph_next[u] >= 0;
+      load_v(u, ph_next[u * NP / NG]);
     }
+#pragma unroll
+    for (int u = 0; u < NP; ++u) ok[u] = ph_next[u] >= 0;
   }
 
   // the four warps' parts, joined in warp order
 #pragma unroll
-  for (int nt = 0; nt < NR; ++nt) {
+  for (int j = 0; j < 2; ++j) {
+    float x = l[j];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      float x = l[nt][j];
+    for (int sh = 4; sh <= 16; sh <<= 1) x += __shfl_xor_sync(0xffffffffu, x, sh);
+    const int row = 2 * c + j;
+    if (r == 0) {
+      st[warp][row][0] = x;
+      st[warp][row][1] = mo[j];
+    }
 #pragma unroll
-      for (int sh = 4; sh <= 16; sh <<= 1) x += __shfl_xor_sync(0xffffffffu, x, sh);
-      const int row = 8 * nt + 2 * c + j;
-      if (r == 0) {
-        st[warp][row][0] = x;
-        st[warp][row][1] = mo[nt][j];
-      }
-#pragma unroll
-      for (int i = 0; i < KS; ++i) {
-        so[warp][row][r * (D / 8) + 2 * i] = o[nt][i][j];
-        so[warp][row][r * (D / 8) + 2 * i + 1] = o[nt][i][2 + j];
-      }
+    for (int i = 0; i < KS; ++i) {
+      so[warp][row][r * (D / 8) + 2 * i] = o[i][j];
+      so[warp][row][r * (D / 8) + 2 * i + 1] = o[i][2 + j];
     }
   }
   __syncthreads();
@@ -422,10 +418,10 @@ attn_decode_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles)
   }
 }
 
-template <int DT, int D, int NR, bool UNI>
+template <int DT, int D, int UNI>
 cudaError_t launch_t(const AttnArgs& a, const AttnParts& p, cudaStream_t st) {
   const int64_t rows = (int64_t)a.max_q * (a.Hq / a.c.H);
-  const int64_t tiles = (rows + 8 * NR - 1) / (8 * NR);
+  const int64_t tiles = (rows + R - 1) / R;
   const int64_t x = tiles * a.b.B * p.splits;
   if (x > INT32_MAX || tiles > INT32_MAX) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
@@ -437,15 +433,14 @@ cudaError_t launch_t(const AttnArgs& a, const AttnParts& p, cudaStream_t st) {
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_decode_kernel<DT, D, NR, UNI>, a, p, (int)tiles);
+  return cudaLaunchKernelEx(&cfg, attn_decode_kernel<DT, D, UNI>, a, p, (int)tiles);
 }
 
 template <int DT, int D>
 cudaError_t launch_d(const AttnArgs& a, const AttnParts& p, cudaStream_t st) {
-  const bool few = (int64_t)a.max_q * (a.Hq / a.c.H) <= 8;
-  if (a.c.bt % 16 == 0)
-    return few ? launch_t<DT, D, 1, true>(a, p, st) : launch_t<DT, D, 2, true>(a, p, st);
-  return few ? launch_t<DT, D, 1, false>(a, p, st) : launch_t<DT, D, 2, false>(a, p, st);
+  if constexpr (D == 64)
+    if (a.c.bt % 32 == 0) return launch_t<DT, D, 32>(a, p, st);
+  return a.c.bt % 16 == 0 ? launch_t<DT, D, 16>(a, p, st) : launch_t<DT, D, 0>(a, p, st);
 }
 
 template <int DT>
@@ -461,10 +456,11 @@ bool attn_decode_takes(int64_t D, int64_t page) {
 
 // CTAs of at least 256 keys, and about sixteen for each of the 148 SMs where the
 // keys are enough for longer ones: a CTA's start and end cost as much as some
-// ten groups of 16 keys of a warp, but few long ones end unevenly (2 x up to
-// 131071 keys of dim 64: 8, 16, 24 CTAs an SM 73, 68, 78 us).
+// ten groups of 16 keys of a warp, but few long ones end unevenly (8, 16, 24 CTAs
+// an SM: 2 x up to 131071 keys of dim 64 58, 57, 67 us, 64 x up to 8192 keys of
+// dim 128 161, 144, 144 us).
 int attn_decode_chunk(int64_t B, int64_t Hkv, int64_t rows, int64_t span) {
-  const int64_t units = std::max<int64_t>(1, B * Hkv * ((rows + 15) / 16));
+  const int64_t units = std::max<int64_t>(1, B * Hkv * ((rows + 7) / 8));
   const int64_t c = units * span / (148 * 16);
   return (int)std::min<int64_t>(1 << 24, std::max<int64_t>(256, (c + 127) / 128 * 128));
 }
