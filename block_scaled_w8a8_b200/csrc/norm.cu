@@ -323,10 +323,14 @@ cudaError_t launch_any(const NormArgs& a, cudaStream_t st) {
 
 template <int DT>
 cudaError_t launch_dt(const NormArgs& a, cudaStream_t st) {
+  // odd widths, strides and groups (4096 x 4096: 90 us, the vector kernel 25 us)
   if (!vec_ok(a)) return launch_any<DT>(a, st);
-  // few rows: a vector a thread, for latency; many: more loads in flight a thread
-  if (a.M <= 148 && a.K <= 8192) return launch_vec<DT, 1>(a, st);
-  if (a.K <= 2048) return launch_vec<DT, 1>(a, st);
+  // Few rows: a vector a thread, for latency; many: more loads in flight a thread
+  // (1, 2 vectors: 16 x 2048 2.4, 2.7 us, 8 x 4096 2.7, 2.9 us, 148 x 8192 3.8, 3.7 us,
+  // 4096 x 2048 15.0, 14.1 us, 4096 x 8192 51, 45 us).  A CTA of 1024 threads ends at
+  // 16384 elements; the wider rows' eight vectors cost up to half more where both
+  // could be taken (4096 x 14336: 117, 75 us), four times less than the other kernel.
+  if (a.M <= 148 && a.K <= 4096) return launch_vec<DT, 1>(a, st);
   return a.K <= 16384 ? launch_vec<DT, 2>(a, st) : launch_vec<DT, 8>(a, st);
 }
 
