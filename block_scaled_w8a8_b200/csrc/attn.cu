@@ -19,81 +19,209 @@ namespace bq {
 
 namespace {
 
+using attn::Range;
 using attn::row_range;
 
-constexpr int kAnyWarps = 4;
+constexpr int kAnyWarps = 4, kAnyRows = 4;
 constexpr int kMaxD = 256;
 
+// Four codes of a row as fp32; `n` of them are there, read at once if `words`.
 template <int DT>
-__device__ __forceinline__ float code_value(uint8_t c) {
-  return DT == kInt8 ? (float)(int8_t)c : e4m3_to_float(c);
+__device__ __forceinline__ void load4(const uint8_t* p, bool words, int n, float (&f)[4]) {
+  uint32_t w = 0, lo, hi;
+  if (words) {
+    w = *reinterpret_cast<const uint32_t*>(p);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < n) w |= (uint32_t)p[e] << (8 * e);
+  }
+  attn::codes_to_f16<DT>(w, lo, hi);
+  const float2 a = __half22float2(reinterpret_cast<const __half2&>(lo));
+  const float2 b = __half22float2(reinterpret_cast<const __half2&>(hi));
+  f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
 }
 
-// A warp per (row, query head): lane l holds dimensions l, l + 32, ...; one
-// key at a time, running maximum and sum in fp32.
+// CUDA cores, any head size, page and alignment.  A CTA works on four rows (tokens x
+// heads of one key head's group) and one part of the keys; a warp takes 32 keys at a
+// time.  Scores: a lane per key, whose codes it reads four at a time where they are
+// aligned, against the four queries in shared memory; values: four dimensions a lane
+// (128 i + 4 lane), the keys in turn.  A code is so read and converted once for four rows.  The
+// softmax runs in fp32, in units of 2^m.  Bound by its instructions, some ten of a
+// warp for a key and row: 1 x 4096 keys, 32 heads over 8, pages of 8: 32 us (12 us where
+// the streaming kernel takes the page), 64 x 2048 keys of dim 80: 265 us, a prompt of
+// 2048 of dim 96: 2.7 ms.
 template <int DT>
-__global__ void __launch_bounds__(kAnyWarps * 32) attn_any_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kAnyWarps * 32)
+attn_any_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles) {
+  __shared__ float4 sq[kMaxD];                           // of the four rows
+  __shared__ float4 sw[kAnyWarps][32];                   // weights of a warp's keys
+  __shared__ int64_t sr[kAnyWarps][32];                  // where their codes lie, or -1
+  __shared__ float so[kAnyWarps][kAnyRows][kMaxD], ss[kAnyWarps][kAnyRows][2];
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int kPer = kMaxD / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t item = (int64_t)blockIdx.x * kAnyWarps + (threadIdx.x >> 5);
-  const int64_t t = item / a.Hq;
-  const int h = (int)(item - t * a.Hq);
-  if (t >= a.b.T) return;
-  const int b = kv::seq_of(a.b, t);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = a.c.D;
+  int idx = (int)blockIdx.x;
+  const int rt = idx % row_tiles;
+  idx /= row_tiles;
+  const int split = idx % parts.splits, b = idx / parts.splits, hk = blockIdx.y;
   kv::Seq s;
   if (!kv::load_seq(a.b, a.c.page, b, s) || s.n > a.max_q || s.len > a.max_kv) {
-    if (lane == 0) record_status(a.status, kStatusBadInput, 0x701u);
+    if (threadIdx.x == 0) record_status(a.status, kStatusBadInput, 0x701u);
     return;
   }
-  if (t < s.row0 || t >= s.row0 + s.n) return;      // a row behind the last sequence
-  int lo, hi;
-  row_range(a, s, (int)(t - s.row0), lo, hi);
-  const int hk = h / (a.Hq / a.c.H), D = a.c.D;
-  const uint16_t* q = a.q + t * a.ldq + h * a.hq;
-  float qv[kPer], o[kPer];
+  const int g = a.Hq / a.c.H, R0 = rt * kAnyRows, n_rows = s.n * g;
+  if (R0 >= n_rows) return;
+  const int i_hi = min(s.n - 1, (R0 + kAnyRows - 1) / g);
+  const Range all = attn::tile_range(a, s, R0 / g, i_hi);
+  const Range part =
+      attn::split_range(all, attn::first_split(a, s, parts.chunk) + split, parts.chunk);
+  if (parts.splits > 1 && part.hi <= part.lo) return;    // the join does not look at it
+  int lo[kAnyRows], hi[kAnyRows];
+  float m[kAnyRows], l[kAnyRows], o[kAnyRows][kPer];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    qv[i] = lane + 32 * i < D ? bf16_bits_to_float(q[lane + 32 * i]) : 0.f;
-    o[i] = 0.f;
+  for (int r = 0; r < kAnyRows; ++r) {
+    // rows behind the last stand in for it: nothing of them is written
+    row_range(a, s, min((R0 + r) / g, s.n - 1), lo[r], hi[r]);
+    m[r] = -INFINITY;
+    l[r] = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) o[r][i] = 0.f;
   }
-  float m = -INFINITY, l = 0.f;
-  for (int j = lo; j < hi; ++j) {
-    const int64_t page = kv::page_of(a.b, a.c, b, j);
-    if (page < 0) {
-      if (lane == 0) record_status(a.status, kStatusBadInput, 0x702u);
-      continue;
+  for (int d = threadIdx.x; d < D; d += kAnyWarps * 32) {
+    float x[kAnyRows];
+#pragma unroll
+    for (int r = 0; r < kAnyRows; ++r) {
+      const int row = min(R0 + r, n_rows - 1);
+      x[r] = bf16_bits_to_float(
+          a.q[(int64_t)(s.row0 + row / g) * a.ldq + (int64_t)(hk * g + row % g) * a.hq + d]);
     }
-    const int64_t ph = page * a.c.H + hk;
-    const int in_page = j % a.c.page;
-    const int64_t row = (ph * a.c.page + in_page) * D;
-    const int64_t blk = ph * (a.c.page / a.c.bt) + in_page / a.c.bt;
-    float d = 0.f;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (lane + 32 * i < D) d = fmaf(qv[i], code_value<DT>(a.c.k[row + lane + 32 * i]), d);
-#pragma unroll
-    for (int o2 = 16; o2 > 0; o2 >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o2);
-    const float sc = d * (a.c.ks[blk] * a.scale);
-    const float mn = fmaxf(m, sc);
-    // a first score of -inf would make the difference below NaN
-    const float base = mn == -INFINITY ? 0.f : mn;
-    const float keep = __expf(m - base), p = __expf(sc - base);
-    l = l * keep + p;
-    const float pv = p * a.c.vs[blk];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (lane + 32 * i < D)
-        o[i] = fmaf(pv, code_value<DT>(a.c.v[row + lane + 32 * i]), o[i] * keep);
-    m = mn;
+    sq[d] = make_float4(x[0], x[1], x[2], x[3]);
   }
-  uint16_t* out = a.out + t * a.ldo + h * a.ho;
-  const float inv = l > 0.f ? __fdiv_rn(1.0f, l) : (l == 0.f ? 0.f : l);   // a NaN stays one
+  __syncthreads();
+  const bool words = D % 4 == 0 && ((reinterpret_cast<uintptr_t>(a.c.k) |
+                                     reinterpret_cast<uintptr_t>(a.c.v)) & 3) == 0;
+  const float scale = a.scale * attn::kLog2e;
+  for (int t = part.lo + 32 * warp; t < part.hi; t += 32 * kAnyWarps) {
+    const int tok = t + lane;
+    int64_t row = -1;
+    float z[kAnyRows] = {}, vs = 0.f;
+    if (tok >= all.lo && tok < part.hi) {
+      const int64_t page = kv::page_of(a.b, a.c, b, tok);
+      if (page < 0) {
+        record_status(a.status, kStatusBadInput, 0x702u);
+      } else {
+        const int64_t ph = page * a.c.H + hk;
+        const int slot = tok % a.c.page;
+        const int64_t blk = ph * (a.c.page / a.c.bt) + slot / a.c.bt;
+        row = (ph * a.c.page + slot) * D;
+        vs = a.c.vs[blk];
+        const uint8_t* k = a.c.k + row;
+#pragma unroll 4
+        for (int d = 0; d < D; d += 4) {
+          float f[4];
+          load4<DT>(k + d, words, D - d, f);
 #pragma unroll
-  for (int i = 0; i < kPer; ++i)
-    if (lane + 32 * i < D) out[lane + 32 * i] = float_to_bf16_bits(o[i] * inv);
-  if (a.lse && lane == 0) a.lse[t * a.Hq + h] = l == 0.f ? -INFINITY : m + logf(l);
+          for (int e = 0; e < 4; ++e) {
+            if (d + e >= D) break;
+            const float4 q = sq[d + e];
+            z[0] = fmaf(q.x, f[e], z[0]);
+            z[1] = fmaf(q.y, f[e], z[1]);
+            z[2] = fmaf(q.z, f[e], z[2]);
+            z[3] = fmaf(q.w, f[e], z[3]);
+          }
+        }
+        const float f = a.c.ks[blk] * scale;
+#pragma unroll
+        for (int r = 0; r < kAnyRows; ++r) z[r] *= f;
+      }
+    }
+    float p[kAnyRows];
+#pragma unroll
+    for (int r = 0; r < kAnyRows; ++r) {
+      if (row < 0 || tok < lo[r] || tok >= hi[r]) z[r] = -INFINITY;
+      const float mn = fmaxf(m[r], warp_max(z[r]));
+      // while every score is -inf the reference is 0, not a difference of infinities
+      const float keep = attn::ex2(m[r] - attn::finite(mn));
+      p[r] = attn::ex2(z[r] - attn::finite(mn));
+      l[r] = fmaf(l[r], keep, p[r]);
+      // a key of weight 0 adds nothing, whatever its value is
+      p[r] = p[r] == 0.f ? 0.f : p[r] * vs;
+      m[r] = mn;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) o[r][i] *= keep;
+    }
+    sw[warp][lane] = make_float4(p[0], p[1], p[2], p[3]);
+    sr[warp][lane] = row;
+    __syncwarp();
+    const int n = min(32, part.hi - t);
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) {
+      const int64_t at = sr[warp][j];
+      if (at < 0) continue;
+      const float4 w = sw[warp][j];
+#pragma unroll
+      for (int i = 0; i < kPer; i += 4) {
+        const int d = 4 * lane + 32 * i;
+        if (d < D) {
+          float f[4];
+          load4<DT>(a.c.v + at + d, words, D - d, f);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (w.x != 0.f) o[0][i + e] = fmaf(w.x, f[e], o[0][i + e]);
+            if (w.y != 0.f) o[1][i + e] = fmaf(w.y, f[e], o[1][i + e]);
+            if (w.z != 0.f) o[2][i + e] = fmaf(w.z, f[e], o[2][i + e]);
+            if (w.w != 0.f) o[3][i + e] = fmaf(w.w, f[e], o[3][i + e]);
+          }
+        }
+      }
+    }
+    __syncwarp();
+  }
+  // the four warps' parts, joined in warp order
+#pragma unroll
+  for (int r = 0; r < kAnyRows; ++r) {
+    float sum = l[r];
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+    if (lane == 0) {
+      ss[warp][r][0] = sum;
+      ss[warp][r][1] = m[r];
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) so[warp][r][4 * lane + 32 * (i & ~3) + (i & 3)] = o[r][i];
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < kAnyRows * D; e += kAnyWarps * 32) {
+    const int r = e / D, d = e % D;
+    if (R0 + r >= n_rows) break;
+    float M = -INFINITY, sum = 0.f, acc = 0.f;
+#pragma unroll
+    for (int w = 0; w < kAnyWarps; ++w) M = fmaxf(M, ss[w][r][1]);
+#pragma unroll
+    for (int w = 0; w < kAnyWarps; ++w) {
+      const float f = attn::ex2(ss[w][r][1] - attn::finite(M));
+      sum = fmaf(ss[w][r][0], f, sum);
+      acc = fmaf(so[w][r][d], f, acc);
+    }
+    const int64_t tok = s.row0 + (R0 + r) / g;
+    const int head = hk * g + (R0 + r) % g;
+    if (parts.splits == 1) {
+      attn::write_row(a, tok, head, d, sum, M, acc);
+    } else {
+      const int64_t at = (tok * a.Hq + head) * parts.splits + split;
+      if (sum != 0.f) parts.o[at * D + d] = acc;
+      if (d == 0) *reinterpret_cast<float2*>(parts.stat + 2 * at) = make_float2(sum, M);
+    }
+  }
+}
+
+// CTAs of at least 128 keys, about sixteen for each of the 148 SMs.
+int attn_any_chunk(int64_t B, int64_t Hkv, int64_t rows, int64_t span) {
+  const int64_t units = std::max<int64_t>(1, B * Hkv * ((rows + kAnyRows - 1) / kAnyRows));
+  const int64_t c = units * span / (148 * 16);
+  return (int)std::min<int64_t>(1 << 24, std::max<int64_t>(128, (c + 127) / 128 * 128));
 }
 
 // Joins the splits of a row: NW warps per (row, query head) take the splits in
@@ -162,11 +290,11 @@ attn_merge_kernel(const AttnArgs a, const AttnParts p) {
 }
 
 template <class... Args>
-cudaError_t launch_pdl(void (*kernel)(Args...), int64_t grid, int threads, cudaStream_t st,
+cudaError_t launch_pdl(void (*kernel)(Args...), dim3 grid, int threads, cudaStream_t st,
                        Args... args) {
-  if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
+  if (grid.x > (unsigned)INT32_MAX) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads);
   cfg.stream = st;
   cudaLaunchAttribute at;
@@ -175,6 +303,16 @@ cudaError_t launch_pdl(void (*kernel)(Args...), int64_t grid, int threads, cudaS
   cfg.attrs = &at;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+cudaError_t launch_any(const AttnArgs& a, const AttnParts& p, cudaStream_t st) {
+  const int64_t rows = (int64_t)a.max_q * (a.Hq / a.c.H);
+  const int64_t tiles = std::max<int64_t>(1, (rows + kAnyRows - 1) / kAnyRows);
+  const dim3 grid((unsigned)std::min<int64_t>(tiles * a.b.B * p.splits, (int64_t)INT32_MAX + 1),
+                  (unsigned)a.c.H);
+  return a.c.dtype == kInt8
+             ? launch_pdl(attn_any_kernel<kInt8>, grid, kAnyWarps * 32, st, a, p, (int)tiles)
+             : launch_pdl(attn_any_kernel<kFp8>, grid, kAnyWarps * 32, st, a, p, (int)tiles);
 }
 
 // The kernel of a call and how it splits the keys, from the call's sizes alone.
@@ -199,6 +337,7 @@ void plan_splits(Path path, int64_t B, int64_t Hq, int64_t Hkv, int64_t max_q, i
   const int64_t g = Hq / Hkv;
   if (path == Path::kTc) p.chunk = attn_tc_chunk(B, Hkv, max_q, g, max_kv);
   if (path == Path::kDecode) p.chunk = attn_decode_chunk(B, Hkv, max_q * g, max_kv);
+  if (path == Path::kAny) p.chunk = attn_any_chunk(B, Hkv, max_q * g, max_kv);
   p.splits = (int)std::max<int64_t>(1, (max_kv + p.chunk - 1) / p.chunk);
 }
 
@@ -214,8 +353,10 @@ size_t attn_workspace_bytes(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64
 
 cudaError_t launch_attn_merge(const AttnArgs& a, const AttnParts& p, cudaStream_t st) {
   const int64_t items = a.b.T * a.Hq;
-  return p.splits <= 4 ? launch_pdl(attn_merge_kernel<1>, (items + 3) / 4, 128, st, a, p)
-                       : launch_pdl(attn_merge_kernel<8>, items, 256, st, a, p);
+  const bool few = p.splits <= 4;
+  const dim3 grid((unsigned)std::min<int64_t>(few ? (items + 3) / 4 : items, (int64_t)INT32_MAX + 1));
+  return few ? launch_pdl(attn_merge_kernel<1>, grid, 128, st, a, p)
+             : launch_pdl(attn_merge_kernel<8>, grid, 256, st, a, p);
 }
 
 cudaError_t launch_kv_attention(const AttnArgs& a, void* ws, cudaStream_t st) {
@@ -223,21 +364,17 @@ cudaError_t launch_kv_attention(const AttnArgs& a, void* ws, cudaStream_t st) {
   const bool aligned = ((reinterpret_cast<uintptr_t>(a.c.k) | reinterpret_cast<uintptr_t>(a.c.v)) &
                         15) == 0;
   const Path path = plan_path(a.c.D, a.c.page, (int64_t)a.max_q * (a.Hq / a.c.H));
-  if (aligned && a.max_q > 0 && path != Path::kAny) {
-    AttnParts p{};
-    plan_splits(path, a.b.B, a.Hq, a.c.H, a.max_q, a.max_kv, p);
-    if (p.splits > 1) {
-      p.stat = static_cast<float*>(ws);
-      p.o = p.stat + (2 * items * p.splits + 3) / 4 * 4;
-    }
-    cudaError_t e =
-        path == Path::kTc ? launch_attn_tc(a, p, st) : launch_attn_decode(a, p, st);
-    if (e == cudaSuccess && p.splits > 1) e = launch_attn_merge(a, p, st);
-    return e;
+  AttnParts p{};
+  plan_splits(path, a.b.B, a.Hq, a.c.H, a.max_q, a.max_kv, p);
+  if (p.splits > 1) {
+    p.stat = static_cast<float*>(ws);
+    p.o = p.stat + (2 * items * p.splits + 3) / 4 * 4;
   }
-  const int64_t grid = (items + kAnyWarps - 1) / kAnyWarps;
-  return a.c.dtype == kInt8 ? launch_pdl(attn_any_kernel<kInt8>, grid, kAnyWarps * 32, st, a)
-                            : launch_pdl(attn_any_kernel<kFp8>, grid, kAnyWarps * 32, st, a);
+  cudaError_t e;
+  if (!aligned || a.max_q == 0 || path == Path::kAny) e = launch_any(a, p, st);
+  else e = path == Path::kTc ? launch_attn_tc(a, p, st) : launch_attn_decode(a, p, st);
+  if (e == cudaSuccess && p.splits > 1) e = launch_attn_merge(a, p, st);
+  return e;
 }
 
 }  // namespace bq
