@@ -879,10 +879,10 @@ static bq_status kv_check(int64_t ld_table, int64_t table_cols, int64_t B, int64
                (long long)page_size);
   BQ_CHECK_ARG(table_cols >= 0 && ld_table >= table_cols, "ld_table must be >= table_cols >= 0");
   if (Hkv > 32767 || page_size > 65536 || D > 16384 || T > INT32_MAX - 1 || B > (1 << 28) ||
-      n_pages > INT32_MAX || table_cols > INT32_MAX / page_size)
+      n_pages > INT32_MAX || table_cols > (1 << 30) / page_size)
     return fail(BQ_ERR_UNSUPPORTED,
-                "the cache calls take Hkv <= 32767, page_size <= 65536, D <= 16384, B <= 2^28 and "
-                "rows, pages and sequence lengths within int32");
+                "the cache calls take Hkv <= 32767, page_size <= 65536, D <= 16384, B <= 2^28, "
+                "table_cols * page_size <= 2^30 and rows and pages within int32");
   return BQ_OK;
 }
 

@@ -18,7 +18,7 @@ __device__ __forceinline__ void row_range(const AttnArgs& a, const kv::Seq& s, i
                                           int& hi) {
   const int pos = s.len - s.n + i;
   hi = a.causal ? min(pos + 1, s.len) : s.len;
-  lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+  lo = a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
 }
 
 // Keys that some row of i_lo .. i_hi sees: both ends grow with the row.

@@ -124,12 +124,13 @@ attn_decode_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles)
   const uint8_t* vbase = a.c.v + 2 * c * D + r * (D / 8);
   int t = part.lo + warp * STEP;
   if (!early) pages(t, part.hi);
-  // (page, key head) of the next round's group u, which begins at token tok, or -1
+  // (page, key head) of the next round's place u, which begins at token tok, or -1;
+  // pages wholly before the first key in sight need not exist
   auto row_of = [&](int u, int tok) -> int64_t {
     if (tok >= part.hi) return -1;
     const int64_t p = pg[0][u];
     if (p >= 0 && p < a.c.n_pages) return p * a.c.H + hk;
-    if (lane == 0) record_status(a.status, kStatusBadInput, 0x712u);
+    if (lane == 0 && tok + TP > all.lo) record_status(a.status, kStatusBadInput, 0x712u);
     return -1;
   };
   Group<D, UNI> G[NG];

@@ -3,8 +3,8 @@
 //
 // A CTA holds 256 rows (tokens x heads of one key head's group) as two tiles of
 // 128 and walks the keys in tiles of 128 tokens:
-//   warps 0-3, 4-7  softmax of row tile 0, 1: a thread per row reads its 128
-//                   scores from tensor memory, writes the weights back as fp16
+//   warps 0-3, 4-7  softmax of row tile 0, 1: a thread per row reads its 64
+//                   scores of a block from tensor memory, writes the weights back as fp16
 //                   over them, and at the end divides the output row;
 //   warps 8-11      keys: codes from memory (requested a tile ahead) to fp16
 //                   tiles in shared memory, twice buffered, and the scales of
@@ -30,6 +30,15 @@
 // Queries are scaled per row by a power of two and exact in fp16, as in
 // attn_decode.cu.  Keys that no row of the CTA sees have zero codes and lg2 vs =
 // -inf, so no stale byte enters a sum.
+//
+// Measured: a prompt of 8192 tokens (32 heads over 8, dim 128) 645 us, 853 TFLOP/s
+// of the two products over the pairs that causality leaves.  Bound by the tensor
+// cores as they are fed: with neither softmax nor conversion in the way the
+// products alone take 508 us, since a score product of 64 keys reads as much of Q
+// from shared memory as one of 128 would.  128 scores at a time halve that, but
+// tensor memory then holds one block a row tile, so that the products wait for the
+// softmax and the other way round (723 us).  The softmax adds 85 us, the conversion
+// 60 us; a CTA's start and end cost about two key tiles of 2.7 us.
 //
 // Every wait is bounded (2 s); on expiry the CTA records a timeout in the
 // device status word, drains its MMAs, frees its tensor memory and exits.

@@ -564,6 +564,7 @@ bq_status bq_rope(const void* x, int64_t ldt, int64_t ldh, const int32_t* positi
  * the kernels alone; entries that cannot be used (offsets that decrease or
  * pass T, a length past table_cols * page_size, a page outside [0, n_pages))
  * are skipped and recorded in the device status word as BQ_ERR_INVALID_ARG.
+ * table_cols * page_size <= 2^30.
  * Rows at and behind seq_offsets[B] are neither read nor written. */
 
 /* Append: quantise the new tokens' keys and values (bf16, element (t, h, d) at
@@ -595,7 +596,8 @@ bq_status bq_kv_attention_workspace_size(int64_t B, int64_t T, int64_t Hq, int64
  *   z_j = scale * (q . k_j),  out = sum_j softmax(z)_j v_j,  lse = ln sum_j exp(z_j)
  * k_j, v_j = code * scale.  Sums and softmax statistics are fp32; out is
  * rounded once to bf16.  A row that sees no key gives zeros and lse = -inf.
- * Slots of a page behind kv_lens[b] may hold any bytes.  The keys and values
+ * Slots of a page behind kv_lens[b] may hold any bytes, and pages that hold only
+ * keys in front of every row's window need not exist (any number in the table).  The keys and values
  * that some row of the call sees, and the queries, must be finite.
  * q: bf16, element (t, h, d) at q[t * ldq + h * hq + d]; out likewise with ldo,
  * ho (no overlap with q); lse: fp32 [T][Hq] or NULL.  max_q_len and max_kv_len

@@ -129,6 +129,7 @@ def append_args(**kw):
     (dict(vs=None), bq.ERR_INVALID_ARG), (dict(table=None), bq.ERR_INVALID_ARG),
     (dict(H=70000), bq.ERR_UNSUPPORTED), (dict(T=1 << 31), bq.ERR_UNSUPPORTED),
     (dict(P=1 << 32), bq.ERR_UNSUPPORTED), (dict(cols=1 << 26, ld=1 << 26), bq.ERR_UNSUPPORTED),
+    (dict(cols=(1 << 24) + 1, ld=1 << 25), bq.ERR_UNSUPPORTED),
     (dict(T=0, k=None), bq.OK), (dict(B=0, off=None), bq.OK)])
 def test_append_refusals(L, kw, status):
     assert L.bq_kv_append(*append_args(**kw)) == status
@@ -536,6 +537,12 @@ ATTN = [  # new, lens, Hq, Hk, D, page, bt, causal, window
     ([150, 40], [400, 41], 4, 2, 64, 64, 64, True, 1),             # a window of itself
     ([190], [450], 6, 2, 128, 128, 1, False, 0),
     ([140, 20], [140, 300], 4, 4, 256, 32, 32, True, 64),
+    ([1, 2], [3000, 900], 6, 2, 96, 24, 8, True, 0),               # split keys, any size of head
+    ([3, 1], [130, 2500], 5, 1, 33, 10, 5, True, 1000),
+    ([2], [4000], 4, 4, 128, 8, 4, True, 0),                       # pages that end inside a tile
+    ([60, 9], [30, 9], 4, 1, 256, 16, 16, True, 2 ** 31 - 1),      # rows before the first key
+    ([6, 9], [3, 9], 2, 1, 64, 16, 16, True, 2 ** 31 - 1),
+    ([200, 9], [130, 9], 4, 2, 128, 64, 16, True, 2 ** 31 - 1),
 ]
 
 
@@ -626,6 +633,162 @@ def test_attention_on_a_side_stream_and_in_a_graph(L):
                 gr.replay()
             for gr, out in graphs:
                 assert torch.equal(out, want)
+
+
+@gpu
+@pytest.mark.parametrize("new,Hq,Hk,D,page,bt", [
+    ([1, 3], 4, 2, 128, 16, 16), ([1, 1], 8, 2, 64, 32, 32), ([2, 1], 4, 2, 96, 24, 8),
+    ([90, 40], 4, 2, 128, 16, 16), ([70, 140], 2, 1, 64, 64, 64)])
+def test_attention_behind_a_window_needs_no_pages(L, new, Hq, Hk, D, page, bt):
+    """Pages that no row sees any more may be gone, and their scales NaN."""
+    g = gen(D + page)
+    lens, window = [1000, 530], 70
+    off, ln, table, count = make_batch(g, new, lens, page)
+    c = random_cache(g, count, Hk, page, D, bt, bq.INT8)
+    q = randn(g, sum(new), Hq, D).bfloat16()
+    want = bq.kv_attention(q, c, off, ln, table, max(new), 1000, window=window)
+    lse = torch.zeros(sum(new), Hq, device="cuda")
+    for b, (n, len_) in enumerate(zip(new, lens)):
+        gone = max(0, len_ - n - window + 1) // page
+        for t in (c.ks, c.vs):
+            t[table[b, :gone].long()] = math.nan
+        table[b, :gone] = -1
+    got = bq.kv_attention(q, c, off, ln, table, max(new), 1000, window=window, lse=lse)
+    bq.check_device_status()
+    assert torch.equal(got, want) and torch.isfinite(lse).all()
+
+
+@gpu
+@pytest.mark.parametrize("new,Hq,Hk,D", [([1, 2], 8, 4, 128), ([80, 1], 8, 4, 128),
+                                         ([1, 2], 8, 4, 96), ([40, 1], 4, 2, 64)])
+def test_attention_takes_codes_at_any_address(L, new, Hq, Hk, D):
+    g = gen(3 * D)
+    off, ln, table, count = make_batch(g, new, [700, 65], 32)
+    c = random_cache(g, count, Hk, 32, D, 16, bq.FP8_E4M3)
+    q = randn(g, sum(new), Hq, D).bfloat16()
+    want, _, tol, _ = ref.attention(q, c.k, c.v, c.ks, c.vs, off, ln, table, bq.FP8_E4M3)
+    for shift in (1, 4, 8):
+        k, v = (torch.empty(t.numel() + 16, dtype=torch.uint8, device="cuda")[shift:shift + t.numel()]
+                .view(t.shape).copy_(t) for t in (c.k, c.v))
+        got = bq.kv_attention(q, c._replace(k=k, v=v), off, ln, table, max(new), 700)
+        assert ((got.double() - want).abs() <= tol).all()
+    bq.check_device_status()
+
+
+@gpu
+@pytest.mark.parametrize("D,new", [(128, 1), (128, 90), (96, 1)])
+def test_cache_past_32_bits(L, D, new):
+    """Pages whose codes lie more than 2^32 bytes into the arrays."""
+    g = gen(D)
+    Hk, page, bt = 8, 64, 16
+    count = (1 << 32) // (Hk * page * D) + 40
+    small = bq.kv_cache(12, Hk, page, D, bt, bq.INT8)
+    big = bq.kv_cache(count, Hk, page, D, bt, bq.INT8)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    lens = [300, new + 3]
+    near = torch.randperm(12, generator=g, device="cuda").to(torch.int32)[:12].view(2, 6)
+    far = near + (count - 12)
+    old = torch.tensor([n - new for n in lens])
+    for upto, n in ((old, old.tolist()), (torch.tensor(lens), [new, new])):
+        off = torch.tensor([0, n[0], sum(n)], **i32)
+        ln = upto.to(**i32)
+        k, v = (randn(g, sum(n), Hk, D).bfloat16() for _ in range(2))
+        bq.kv_append(small, k, v, off, ln, near)
+        bq.kv_append(big, k, v, off, ln, far)
+    for a, b in zip(small[:4], big[:4]):
+        assert torch.equal(a, b[count - 12:]) and int((b[:count - 12] != 0).sum()) == 0
+    q = randn(g, 2 * new, 2 * Hk, D).bfloat16()
+    assert torch.equal(bq.kv_attention(q, small, off, ln, near, new, 400),
+                       bq.kv_attention(q, big, off, ln, far, new, 400))
+    bq.check_device_status()
+
+
+@gpu
+def test_a_batch_of_many_sequences(L):
+    """More sequences than a warp counts side by side, some of them with nothing new."""
+    g = gen(23)
+    B, H, D, page, bt = 1500, 1, 64, 16, 8
+    new = [(i * 7) % 3 for i in range(B)]
+    lens = [n + (i * 5) % 29 for i, n in enumerate(new)]
+    off, ln, table, count = make_batch(g, new, lens, page)
+    c = random_cache(g, count, H, page, D, bt, bq.INT8)
+    k, v = (randn(g, sum(new) + 2, H, D).bfloat16() for _ in range(2))
+    want = [ref.append(a, s, t, off, ln, table, bq.INT8) for a, s, t in ((c.k, c.ks, k), (c.v, c.vs, v))]
+    bq.kv_append(c, k, v, off, ln, table)
+    assert torch.equal(c.k, want[0][0]) and torch.equal(c.v, want[1][0])
+    assert torch.equal(c.ks, want[0][1]) and torch.equal(c.vs, want[1][1])
+    q = randn(g, sum(new), 2, D).bfloat16()
+    out = bq.kv_attention(q, c, off, ln, table, 2, 40)
+    want, _, tol, _ = ref.attention(q, c.k, c.v, c.ks, c.vs, off, ln, table, bq.INT8)
+    assert ((out.double() - want).abs() <= tol).all()
+    bq.check_device_status()
+
+
+@gpu
+def test_norm_rope_and_append_in_a_graph(L):
+    """Captured once, replayed with other inputs, against the same calls made eagerly."""
+    g = gen(29)
+    H, D, T = 2, 128, 9
+    x, res = randn(g, T, 512).bfloat16(), randn(g, T, 512).bfloat16()
+    w = (1 + 0.1 * randn(g, 512)).bfloat16()
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    turns, ms = bq.rope_frequencies(D)
+    off, ln, table, count = make_batch(g, [4, 5], [30, 20], 16)
+    start = random_cache(g, count, H, 16, D, 8, bq.FP8_E4M3)
+    c = bq.kv_cache(count, H, 16, D, 8, bq.FP8_E4M3)
+    k, v = (randn(g, T, H, D).bfloat16() for _ in range(2))
+
+    def step(out):
+        q8, s, r = bq.rmsnorm_quant(x, w, residual=res, dtype=bq.FP8_E4M3)
+        m8, m = bq.mx_rmsnorm_quant(x, w)[:2]
+        bq.rope(k, pos, turns, mscale=ms, out=out)
+        bq.kv_append(c, out, v, off, ln, table)
+        return q8, s, r, m8, m
+
+    turned = torch.empty_like(k)
+    step(turned)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kept = step(turned)
+    for i in range(2):
+        for t in (x, res, k, v):
+            t.copy_(randn(g, *t.shape).bfloat16())
+        pos.add_(100 * i)
+        ln.sub_(i)
+        for a, b in zip(c[:4], start[:4]):
+            a.copy_(b)
+        graph.replay()
+        got = [t.clone() for t in (*kept, turned, *c[:4])]
+        for a, b in zip(c[:4], start[:4]):
+            a.copy_(b)
+        eager = torch.empty_like(k)
+        want = (*step(eager), eager, *c[:4])
+        # the atoms of rows that are not there hold what they held
+        for n, (a, b) in enumerate(zip(got, want)):
+            if n != 4:
+                assert torch.equal(a, b), n
+    bq.check_device_status()
+
+
+@gpu
+def test_two_calls_at_once(L):
+    """Calls on two streams, each with a workspace of its own."""
+    g = gen(31)
+    page, Hk, D = 32, 2, 128
+    for new, lens in (([1, 1], [5000, 70]), ([300, 1], [2000, 90])):
+        off, ln, table, count = make_batch(g, new, lens, page)
+        c = random_cache(g, count, Hk, page, D, 16, bq.INT8)
+        qs = [randn(g, sum(new), 8, D).bfloat16() for _ in range(2)]
+        want = [bq.kv_attention(q, c, off, ln, table, max(new), 5000) for q in qs]
+        streams = [torch.cuda.Stream() for _ in qs]
+        for _ in range(5):
+            got = []
+            for st, q in zip(streams, qs):
+                st.wait_stream(torch.cuda.current_stream())
+                with torch.cuda.stream(st):
+                    got.append(bq.kv_attention(q, c, off, ln, table, max(new), 5000))
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
 @gpu
