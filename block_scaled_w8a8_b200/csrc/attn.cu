@@ -75,8 +75,7 @@ attn_any_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles) {
   if (R0 >= n_rows) return;
   const int i_hi = min(s.n - 1, (R0 + kAnyRows - 1) / g);
   const Range all = attn::tile_range(a, s, R0 / g, i_hi);
-  const Range part =
-      attn::split_range(all, attn::first_split(a, s, parts.chunk) + split, parts.chunk);
+  const Range part = attn::split_range(all, attn::split_base(a, s), split, parts.chunk);
   if (parts.splits > 1 && part.hi <= part.lo) return;    // the join does not look at it
   int lo[kAnyRows], hi[kAnyRows];
   float m[kAnyRows], l[kAnyRows], o[kAnyRows][kPer];
@@ -249,9 +248,9 @@ attn_merge_kernel(const AttnArgs a, const AttnParts p) {
   // the splits that hold keys this row sees
   int lo, hi;
   row_range(a, s, (int)(t - s.row0), lo, hi);
-  const int first = attn::first_split(a, s, p.chunk);
-  const int i0 = hi > lo ? lo / p.chunk - first : 0;
-  const int i1 = hi > lo ? (hi - 1) / p.chunk - first + 1 : 0;
+  const int base = attn::split_base(a, s);
+  const int i0 = hi > lo ? (lo - base) / p.chunk : 0;
+  const int i1 = hi > lo ? (hi - 1 - base) / p.chunk + 1 : 0;
   float mo = -INFINITY;
   for (int i = i0 + lane; i < i1; i += 32) mo = fmaxf(mo, stat[i].y);
   mo = warp_max(mo);
@@ -329,16 +328,26 @@ Path plan_path(int64_t D, int64_t page, int64_t rows) {
   return attn_decode_takes(D, page) ? Path::kDecode : Path::kAny;
 }
 
-// Chunk of keys and most chunks that the keys of one sequence's rows lie in.
+// Chunk of keys, and how many chunks the keys of one sequence's rows lie in.  With a
+// window they are a stretch of window + max_q keys; it is split as finely as the
+// workspace, which knows of no window, has room for.
 void plan_splits(Path path, int64_t B, int64_t Hq, int64_t Hkv, int64_t max_q, int64_t max_kv,
-                 AttnParts& p) {
-  p.splits = 1;
-  p.chunk = 1 << 30;
+                 int64_t window, AttnParts& p) {
   const int64_t g = Hq / Hkv;
-  if (path == Path::kTc) p.chunk = attn_tc_chunk(B, Hkv, max_q, g, max_kv);
-  if (path == Path::kDecode) p.chunk = attn_decode_chunk(B, Hkv, max_q * g, max_kv);
-  if (path == Path::kAny) p.chunk = attn_any_chunk(B, Hkv, max_q * g, max_kv);
-  p.splits = (int)std::max<int64_t>(1, (max_kv + p.chunk - 1) / p.chunk);
+  auto plan = [&](int64_t span) {
+    p.chunk = path == Path::kTc       ? attn_tc_chunk(B, Hkv, max_q, g, span)
+              : path == Path::kDecode ? attn_decode_chunk(B, Hkv, max_q * g, span)
+                                      : attn_any_chunk(B, Hkv, max_q * g, span);
+    p.splits = (int)std::max<int64_t>(1, (span + p.chunk - 1) / p.chunk);
+  };
+  plan(max_kv);
+  const int64_t seen = window + max_q + 127;      // from a multiple of 128 on
+  if (window == 0 || seen >= max_kv) return;
+  const int64_t most = p.splits;
+  plan(seen);
+  if (p.splits <= most) return;
+  p.chunk = (int)(((seen + most - 1) / most + 127) / 128 * 128);
+  p.splits = (int)((seen + p.chunk - 1) / p.chunk);
 }
 
 }  // namespace
@@ -347,7 +356,7 @@ size_t attn_workspace_bytes(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64
                             int64_t max_q, int64_t max_kv, int64_t page, int64_t bt) {
   (void)bt;
   AttnParts p{};
-  plan_splits(plan_path(D, page, max_q * (Hq / Hkv)), B, Hq, Hkv, max_q, max_kv, p);
+  plan_splits(plan_path(D, page, max_q * (Hq / Hkv)), B, Hq, Hkv, max_q, max_kv, 0, p);
   return attn_part_bytes(T * Hq, p.splits, D);
 }
 
@@ -365,7 +374,7 @@ cudaError_t launch_kv_attention(const AttnArgs& a, void* ws, cudaStream_t st) {
                         15) == 0;
   const Path path = plan_path(a.c.D, a.c.page, (int64_t)a.max_q * (a.Hq / a.c.H));
   AttnParts p{};
-  plan_splits(path, a.b.B, a.Hq, a.c.H, a.max_q, a.max_kv, p);
+  plan_splits(path, a.b.B, a.Hq, a.c.H, a.max_q, a.max_kv, a.window, p);
   if (p.splits > 1) {
     p.stat = static_cast<float*>(ws);
     p.o = p.stat + (2 * items * p.splits + 3) / 4 * 4;

@@ -32,21 +32,21 @@ __device__ __forceinline__ Range tile_range(const AttnArgs& a, const kv::Seq& s,
   return r;
 }
 
-// Keys are split at the multiples of `chunk` tokens, counted from the one that
-// holds the first key any row of the sequence sees.
-__device__ __forceinline__ int first_split(const AttnArgs& a, const kv::Seq& s, int chunk) {
+// Where the keys of a sequence begin to be split, in chunks of `chunk` tokens: the
+// first key that any row of it sees, rounded down to the 128 keys of a tile.
+__device__ __forceinline__ int split_base(const AttnArgs& a, const kv::Seq& s) {
   int lo, hi;
   row_range(a, s, 0, lo, hi);
-  return lo / chunk;
+  return lo / 128 * 128;
 }
 
-// The keys of `all` in chunk number i; may be empty.  A chunk is a multiple of
-// the kernels' key tiles, and so is the start, but for that of `all` itself,
-// which is rounded down to the 128 keys of a tile.
-__device__ __forceinline__ Range split_range(const Range& all, int i, int chunk) {
+// The keys of `all` in chunk number i; may be empty.  A chunk is a multiple of the
+// kernels' key tiles, and so is its start, that of `all` rounded down included.
+__device__ __forceinline__ Range split_range(const Range& all, int base, int i, int chunk) {
   Range r;
-  r.lo = (int)max((int64_t)all.lo / 128 * 128, (int64_t)i * chunk);
-  r.hi = (int)min((int64_t)all.hi, ((int64_t)i + 1) * chunk);
+  const int64_t lo = base + (int64_t)i * chunk;
+  r.lo = (int)max((int64_t)all.lo / 128 * 128, min(lo, (int64_t)all.hi));
+  r.hi = (int)min((int64_t)all.hi, lo + chunk);
   return r;
 }
 

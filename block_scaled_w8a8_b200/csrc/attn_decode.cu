@@ -114,7 +114,7 @@ attn_decode_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles)
   // keys that some row of this tile sees, and this split's part of them
   const int i_lo = R0 / g, i_hi = min(s.n - 1, (R0 + R - 1) / g);
   const Range all = tile_range(a, s, i_lo, i_hi);
-  const Range part = split_range(all, first_split(a, s, parts.chunk) + split, parts.chunk);
+  const Range part = split_range(all, split_base(a, s), split, parts.chunk);
   if (parts.splits > 1 && part.hi <= part.lo) return;      // the join does not look at it
 
   const int bt = a.c.bt, nblk = page / bt;
@@ -455,15 +455,21 @@ bool attn_decode_takes(int64_t D, int64_t page) {
   return (D == 64 || D == 128) && page % 16 == 0;
 }
 
-// CTAs of at least 256 keys, and about sixteen for each of the 148 SMs where the
-// keys are enough for longer ones: a CTA's start and end cost as much as some
-// ten groups of 16 keys of a warp, but few long ones end unevenly (8, 16, 24 CTAs
-// an SM: 2 x up to 131071 keys of dim 64 58, 57, 67 us, 64 x up to 8192 keys of
-// dim 128 161, 144, 144 us).
+// Long keys: about sixteen CTAs for each of the 148 SMs.  A CTA's start and end cost
+// as much as some ten groups of 16 keys of a warp, but few long ones end unevenly
+// (8, 16, 24 CTAs an SM: 2 x up to 131071 keys of dim 64 58, 57, 67 us, 64 x up to
+// 8192 keys of dim 128 161, 144, 144 us).  Where that would leave a CTA 512 keys or
+// fewer, as many as run at once, four an SM, with 256 to 1152 keys each (chunks of 256,
+// 512, 1152: 64 x 1152 keys 56, 46, 32 us, 32 x 1001 keys 30, 25, 30 us, 4 x 2001 keys
+// 15, 19, 23 us).
 int attn_decode_chunk(int64_t B, int64_t Hkv, int64_t rows, int64_t span) {
   const int64_t units = std::max<int64_t>(1, B * Hkv * ((rows + 7) / 8));
-  const int64_t c = units * span / (148 * 16);
-  return (int)std::min<int64_t>(1 << 24, std::max<int64_t>(256, (c + 127) / 128 * 128));
+  int64_t c = units * span / (148 * 16);
+  if (c <= 512) {
+    const int64_t parts = std::max<int64_t>(1, 148 * 4 / units);
+    c = std::min<int64_t>(1152, std::max<int64_t>(256, (span + parts - 1) / parts));
+  }
+  return (int)std::min<int64_t>(1 << 24, (c + 127) / 128 * 128);
 }
 
 cudaError_t launch_attn_decode(const AttnArgs& a, const AttnParts& p, cudaStream_t st) {

@@ -238,7 +238,7 @@ attn_tc_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles) {
   const bool two = R0 + BM < n_rows;      // the second row tile has rows
   const int i_lo = R0 / g, i_hi = min(s.n - 1, (R0 + 2 * BM - 1) / g);
   const Range all = tile_range(a, s, i_lo, i_hi);
-  const Range part = split_range(all, first_split(a, s, parts.chunk) + split, parts.chunk);
+  const Range part = split_range(all, split_base(a, s), split, parts.chunk);
   if (parts.splits > 1 && part.hi <= part.lo) return;      // the join does not look at it
   const int keys = max(part.hi - part.lo, 0);
   const int nt = (keys + BN - 1) / BN, nb = (keys + SN - 1) / SN;   // key tiles, score blocks

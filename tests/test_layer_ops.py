@@ -543,6 +543,10 @@ ATTN = [  # new, lens, Hq, Hk, D, page, bt, causal, window
     ([60, 9], [30, 9], 4, 1, 256, 16, 16, True, 2 ** 31 - 1),      # rows before the first key
     ([6, 9], [3, 9], 2, 1, 64, 16, 16, True, 2 ** 31 - 1),
     ([200, 9], [130, 9], 4, 2, 128, 64, 16, True, 2 ** 31 - 1),
+    ([1, 2], [6000, 300], 4, 2, 128, 64, 16, True, 2000),          # a window of split keys
+    ([3], [5001], 2, 2, 64, 32, 32, True, 1),
+    ([300, 40], [5000, 1000], 4, 2, 128, 64, 16, True, 1500),
+    ([2], [3001], 2, 1, 80, 16, 8, True, 1200),
 ]
 
 
