@@ -225,7 +225,9 @@ int attn_any_chunk(int64_t B, int64_t Hkv, int64_t rows, int64_t span) {
 
 // Joins the splits of a row: NW warps per (row, query head) take the splits in
 // turn, and their sums are joined in warp order.  NW = 1 up to 4 splits, 8 above:
-// the splits' rows are loaded side by side instead of one latency each.
+// the splits' rows are loaded side by side instead of one latency each (attention and
+// join, 1, 8 warps: 32 rows of 16 splits 23, 13 us; 512 rows of 4 25, 24 us; 49248 rows of
+// 2 173, 288 us).
 template <int NW>
 __global__ void __launch_bounds__(128 * (NW > 4 ? 2 : 1))
 attn_merge_kernel(const AttnArgs a, const AttnParts p) {

@@ -156,7 +156,8 @@ __device__ __forceinline__ uint32_t pack4_recip(const float v[4], float s, float
 // and kept in registers between the maximum and the codes.  A CTA has as many such
 // items as make about 256 threads, each with a barrier of its own.  What bounds
 // it is the chain of loads (lengths, rows and page, scale), so both arrays go
-// through it together.
+// through it together.  64 tokens x 8 heads of 128: 5.2 us (one item a CTA: 6.1 us);
+// four prompts of up to 2731 tokens: 17.5 us, 3.1 TB/s.
 constexpr int kVecs = 4;
 constexpr int kVecThreads = 512;
 
