@@ -55,6 +55,30 @@ __device__ __forceinline__ void weighted(const uint4& r, const uint4& w, float w
   }
 }
 
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// a / b from r near 1 / b: the quotient's remainder is exact in one FMA, and the
+// quotient corrected by it is off by less than one last place (Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor",
+// 1990).  For operands far from the ends of fp32.
+__device__ __forceinline__ float quotient(float a, float b, float r) {
+  const float q = a * r;
+  return fmaf(fmaf(-q, b, a), r, q);
+}
+
+// 1 / sqrt(x): a Newton step on the approximation, its residual 1 - x r^2 with the
+// rounding of x r put back.
+__device__ __forceinline__ float inv_sqrt(float x) {
+  if (!(x >= 0x1p-100f && x <= 0x1p100f)) return __fdiv_rn(1.0f, __fsqrt_rn(x));
+  const float r = rsqrtf(x), h = x * r;
+  const float e = fmaf(-fmaf(x, r, -h), r, fmaf(-h, r, 1.0f));
+  return fmaf(0.5f * r, e, r);
+}
+
 // Four codes of y * inv, |y * inv| <= 127 (1 + 2^-22): round to nearest even.
 __device__ __forceinline__ uint32_t int8x4(const float* y, float inv) {
   uint32_t b[4];
@@ -204,7 +228,7 @@ norm_vec_kernel(const NormArgs a, const int lpg) {       // lpg: lanes of a grou
     __syncthreads();
     sum = lane < nw ? red[parity][0][lane] : 0.f;
     sum = warp_sum(sum);
-    const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(fmaf(sum, inv_k, a.eps)));
+    const float rstd = inv_sqrt(fmaf(sum, inv_k, a.eps));
     float row_max = 0.f;
     if (lpg == 0) {
 #pragma unroll
@@ -245,12 +269,16 @@ norm_vec_kernel(const NormArgs a, const int lpg) {       // lpg: lanes of a grou
         q.y = e4m3x4(y + 4, inv);
         if (first) a.sf[mx_sf_index(m, g, a.K)] = (uint8_t)(se + 127);
       } else {
-        const float sc = group_scale<DT>(amax * rstd);
-        if (amax >= 0x1p-100f && amax <= 0x1p100f) {
-          const float f = __fdiv_rn(DT == kInt8 ? 127.0f : 448.0f, amax);
+        constexpr float kQ = DT == kInt8 ? 127.0f : 448.0f;
+        const float top = amax * rstd;
+        float sc;
+        if (fminf(amax, top) >= 0x1p-100f && fmaxf(amax, top) <= 0x1p100f) {
+          sc = quotient(top, kQ, 1.0f / kQ);
+          const float f = quotient(kQ, amax, rcp(amax));
           q.x = DT == kInt8 ? int8x4(t, f) : e4m3x4(t, f);
           q.y = DT == kInt8 ? int8x4(t + 4, f) : e4m3x4(t + 4, f);
         } else {                               // the factor may not be a number
+          sc = group_scale<DT>(top);
           float y[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) y[e] = t[e] * rstd;
