@@ -12,6 +12,7 @@
 
 #include "bq_common.cuh"
 #include "layer_ops.h"
+#include "sm100.cuh"
 
 namespace bq {
 
@@ -42,16 +43,30 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
+// Two fp32 in one register pair, for the instructions that take two.
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
+  return (uint64_t)hi << 32 | lo;
+}
+__device__ __forceinline__ uint64_t both(uint32_t bf16x2) {
+  return pair(bf16x2 << 16, bf16x2 & 0xFFFF0000u);
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 // t = r (w + w_off) of eight elements, r and w as packed bf16: exact in fp32 for
 // w_off = 0.
 __device__ __forceinline__ void weighted(const uint4& r, const uint4& w, float w_off,
                                          float (&t)[8]) {
   const uint32_t rr[4] = {r.x, r.y, r.z, r.w}, ww[4] = {w.x, w.y, w.z, w.w};
+  const uint64_t off = pair(__float_as_uint(w_off), __float_as_uint(w_off));
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    t[2 * e] = __uint_as_float(rr[e] << 16) * (__uint_as_float(ww[e] << 16) + w_off);
-    t[2 * e + 1] = __uint_as_float(rr[e] & 0xFFFF0000u) *
-                   (__uint_as_float(ww[e] & 0xFFFF0000u) + w_off);
+    const uint64_t x = mul2(both(rr[e]), sm100::add2(both(ww[e]), off));
+    t[2 * e] = __uint_as_float((uint32_t)x);
+    t[2 * e + 1] = __uint_as_float((uint32_t)(x >> 32));
   }
 }
 
@@ -156,8 +171,9 @@ __global__ void __launch_bounds__(kAnyThreads) norm_any_kernel(const NormArgs a)
 // the whole row): a CTA per row, V vectors of 8 elements a thread, everything in
 // registers, one barrier a row.  Memory-bound: x and the residual are read once,
 // the sum, the codes and the scales written once; the next row is under way while
-// one is reduced (up to 16384 columns).  With a residual, 4096 x 4096 to INT8: 24.5 us,
-// 4.8 TB/s; 2047 x 14336 to MXFP8: 36.6 us, 5.6 TB/s.  In place is safe: a row is loaded
+// one is reduced (up to 16384 columns).  With a residual, 4096 x 4096 to INT8: 23.7 us,
+// 5.0 TB/s; 2047 x 14336 to MXFP8: 36.1 us, 5.7 TB/s: what it issues (three quarters
+// of the issue slots) stands in the way of the rest.  In place is safe: a row is loaded
 // and stored by one CTA, each element by one thread, loads first.
 //
 // y = t rstd with t = r (w + w_off), and rstd falls out of y / s: the codes are those
@@ -205,7 +221,7 @@ norm_vec_kernel(const NormArgs a, const int lpg) {       // lpg: lanes of a grou
       sv[i] = ns[i];
     }
     if (kAhead && m + gridDim.x < a.M) load(m + gridDim.x);
-    float sum = 0.f;
+    uint64_t sums = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       uint32_t* r = reinterpret_cast<uint32_t*>(&rv[i]);
@@ -213,17 +229,15 @@ norm_vec_kernel(const NormArgs a, const int lpg) {       // lpg: lanes of a grou
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         if (a.res) {
-          const float lo = __uint_as_float(r[e] << 16) + __uint_as_float(t[e] << 16);
-          const float hi = __uint_as_float(r[e] & 0xFFFF0000u) + __uint_as_float(t[e] & 0xFFFF0000u);
-          r[e] = pack_bf16(lo, hi);
+          const uint64_t x = sm100::add2(both(r[e]), both(t[e]));
+          r[e] = pack_bf16(__uint_as_float((uint32_t)x), __uint_as_float((uint32_t)(x >> 32)));
         }
-        const float lo = __uint_as_float(r[e] << 16), hi = __uint_as_float(r[e] & 0xFFFF0000u);
-        sum = fmaf(lo, lo, fmaf(hi, hi, sum));
+        sums = sm100::fma2(both(r[e]), both(r[e]), sums);
       }
       const int v = i * nt + tid;
       if (a.res_out && v < nvec) reinterpret_cast<uint4*>(a.res_out + m * a.ldro)[v] = rv[i];
     }
-    sum = warp_sum(sum);
+    float sum = warp_sum(__uint_as_float((uint32_t)sums) + __uint_as_float((uint32_t)(sums >> 32)));
     if (lane == 0) red[parity][0][warp] = sum;
     __syncthreads();
     sum = lane < nw ? red[parity][0][lane] : 0.f;
@@ -352,13 +366,14 @@ cudaError_t launch_any(const NormArgs& a, cudaStream_t st) {
 
 template <int DT>
 cudaError_t launch_dt(const NormArgs& a, cudaStream_t st) {
-  // odd widths, strides and groups (4096 x 4096: 90 us, the vector kernel 25 us)
+  // odd widths, strides and groups (4096 x 4096: 89 us, the vector kernel 24 us)
   if (!vec_ok(a)) return launch_any<DT>(a, st);
   // Few rows: a vector a thread, for latency; many: more loads in flight a thread
-  // (1, 2 vectors: 16 x 2048 2.4, 2.7 us, 8 x 4096 2.7, 2.9 us, 148 x 8192 3.8, 3.7 us,
-  // 4096 x 2048 15.0, 14.1 us, 4096 x 8192 51, 45 us).  A CTA of 1024 threads ends at
+  // (1, 2 vectors: 16 x 2048 2.2, 2.6 us, 148 x 4096 2.7, 2.9 us, 148 x 8192 3.6, 3.4 us,
+  // 4096 x 2048 14.0, 13.7 us, 4096 x 8192 46, 43 us).  A CTA of 1024 threads ends at
   // 16384 elements; the wider rows' eight vectors cost up to half more where both
-  // could be taken (4096 x 14336: 117, 75 us), four times less than the other kernel.
+  // could be taken (4096 x 14336: 111, 74 us), a sixth of the other kernel's time (2048 x
+  // 32768: 116, 682 us).
   if (a.M <= 148 && a.K <= 4096) return launch_vec<DT, 1>(a, st);
   return a.K <= 16384 ? launch_vec<DT, 2>(a, st) : launch_vec<DT, 8>(a, st);
 }
