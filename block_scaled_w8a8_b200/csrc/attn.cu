@@ -365,7 +365,8 @@ size_t attn_workspace_bytes(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64
 cudaError_t launch_attn_merge(const AttnArgs& a, const AttnParts& p, cudaStream_t st) {
   const int64_t items = a.b.T * a.Hq;
   const bool few = p.splits <= 4;
-  const dim3 grid((unsigned)std::min<int64_t>(few ? (items + 3) / 4 : items, (int64_t)INT32_MAX + 1));
+  const int64_t ctas = few ? (items + 3) / 4 : items;
+  const dim3 grid((unsigned)std::min<int64_t>(ctas, (int64_t)INT32_MAX + 1));
   return few ? launch_pdl(attn_merge_kernel<1>, grid, 128, st, a, p)
              : launch_pdl(attn_merge_kernel<8>, grid, 256, st, a, p);
 }

@@ -249,7 +249,8 @@ attn_tc_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles) {
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBar);
   uint64_t *k_full = bars, *v_full = bars + 2, *k_empty = bars + 4, *v_empty = bars + 6,
            *sc_full = bars + 8, *s_full = bars + 12, *p_ready = bars + 16, *o_done = bars + 20,
-           *drain = bars + 22, *q_full = bars + 23, *o_last = bars + 25;   // s_full, p_ready: [row tile][block & 1]
+           *drain = bars + 22, *q_full = bars + 23, *o_last = bars + 25;
+  // s_full, p_ready: [row tile][block & 1]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + L::kNumBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -526,7 +527,8 @@ attn_tc_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles) {
            wait_bar(&s_full[2 * t + (i & 1)], j & 1, abort_flag, a.status, 0x739u);
       if (!ok) break;
       tc_fence_after();
-      // UNI: the block's four groups; otherwise its 64 entries of each of three arrays
+      // UNI: the block's four groups (alike with 64); otherwise its 64 entries of each of
+      // three arrays
       const float4* sc4 =
           reinterpret_cast<const float4*>(smem + L::kSc + (uint32_t)(j & 3) * L::kScSlot) +
           (UNI ? 4 : SN / 4) * (i & 1);

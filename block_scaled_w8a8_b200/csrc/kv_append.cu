@@ -162,7 +162,8 @@ constexpr int kVecs = 4;
 constexpr int kVecThreads = 512;
 
 template <int DT>
-__global__ void __launch_bounds__(kVecThreads, 1) append_vec_kernel(const AppendArgs a, const int NW) {
+__global__ void __launch_bounds__(kVecThreads, 1)
+append_vec_kernel(const AppendArgs a, const int NW) {
   __shared__ float red[2][kVecThreads / 32];
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -266,7 +267,9 @@ __global__ void __launch_bounds__(kVecThreads, 1) append_vec_kernel(const Append
 }
 
 bool vec_ok(const AppendArgs& a) {
-  auto al = [](const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; };
+  auto al = [](const void* p, uintptr_t n) {
+    return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0;
+  };
   return a.c.D % 8 == 0 && (int64_t)a.c.bt * a.c.D <= 8 * kVecs * kVecThreads && al(a.k, 16) &&
          al(a.v, 16) && al(a.c.k, 8) && al(a.c.v, 8) && a.ldk % 8 == 0 && a.hk % 8 == 0 &&
          a.ldv % 8 == 0 && a.hv % 8 == 0;

@@ -106,7 +106,8 @@ __global__ void __launch_bounds__(kVecThreads) rope_vec_kernel(const RopeArgs a,
       const int h = hb + i * lanes;
       if (h >= H) break;
       va[i] = *reinterpret_cast<const uint4*>(xt + h * a.ldh);
-      if (!INTER && !copy) vb[INTER ? 0 : i] = *reinterpret_cast<const uint4*>(xt + h * a.ldh + half);
+      if (!INTER && !copy)
+        vb[INTER ? 0 : i] = *reinterpret_cast<const uint4*>(xt + h * a.ldh + half);
     }
   };
   if (on) load(first, h0);                     // under way while the angles are formed
@@ -138,7 +139,8 @@ __global__ void __launch_bounds__(kVecThreads) rope_vec_kernel(const RopeArgs a,
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const float4 q = f[INTER ? k >> 1 : k];
-            const float a0 = __uint_as_float(wa[k] << 16), a1 = __uint_as_float(wa[k] & 0xFFFF0000u);
+            const float a0 = __uint_as_float(wa[k] << 16);
+            const float a1 = __uint_as_float(wa[k] & 0xFFFF0000u);
             if (INTER) {
               const float c = k & 1 ? q.z : q.x, s = k & 1 ? q.w : q.y;
               wa[k] = pack_bf16(turned_a(a0, a1, c, s), turned_b(a0, a1, c, s));
@@ -161,8 +163,8 @@ bool vec_ok(const RopeArgs& a) {
   auto al = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
   const int64_t unit = a.interleaved ? 8 : 16;           // of rot
   return al(a.x) && al(a.out) && a.ldt % 8 == 0 && a.ldh % 8 == 0 && a.ldot % 8 == 0 &&
-         a.ldoh % 8 == 0 && a.D % 8 == 0 && a.rot % unit == 0 && a.D <= 1024 && a.D >= 8 && (a.rot > 0 || a.out != a.x) &&
-         a.H * a.D <= (1 << 22);
+         a.ldoh % 8 == 0 && a.D % 8 == 0 && a.rot % unit == 0 && a.D <= 1024 && a.D >= 8 &&
+         (a.rot > 0 || a.out != a.x) && a.H * a.D <= (1 << 22);
 }
 
 }  // namespace
