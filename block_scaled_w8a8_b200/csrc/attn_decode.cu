@@ -25,12 +25,14 @@
 // fp16 number 1024 + 128 + q; e4m3: the hardware conversion).  A query row is
 // scaled by a power of two to a largest magnitude of 2^14 .. 2^15 and is then
 // exact in fp16 too (8 significant bits), but for elements below 2^-29 of the
-// row's largest.  Scores and sums are fp32.  The weights are rounded to fp16
-// (half a step: 2^-11); as in attn_tc.cu they include the value's block scale,
-// 2^(y - mo) with y = z + lg2 vs, and l += weight / vs.  mo is the row's largest y
-// of the first keys a warp sees; later weights are formed with it as it stands,
-// and only where one passes 2^10 (fp16 ends at 2^16) is mo raised and O rescaled,
-// so that a group of keys costs no search for a maximum across lanes.
+// row's largest.  Scores and sums are fp32.  The weights are rounded to fp16; as in
+// attn_tc.cu they include the value's block scale, 2^(y - mo) with y = z + lg2 vs,
+// and l += weight / vs.  mo is set 11 below the row's largest y of the first keys a
+// warp sees; later weights are formed with it as it stands, and only where one passes
+// 2^15 (fp16 ends at 2^16) is mo raised and O rescaled, so that a group of keys
+// costs no search for a maximum across lanes.  A weight is so off by at most half a
+// step (2^-11 of it) within 2^-25 of the row's largest, and by at most 2^-36 of the
+// largest below that.
 // Masked weights are set to zero, and the codes of values outside the rows'
 // range are replaced by zero before the product, so no stale byte enters a sum.
 #include <algorithm>
@@ -47,6 +49,9 @@ namespace {
 using namespace attn;
 
 constexpr int kWarps = 4, R = 8;        // R: rows of a CTA
+// The reference of a row is set kBelow (log2) under the largest y, and raised when y
+// passes it by kTop: see the precision note above.
+constexpr float kBelow = 11.0f, kTop = 15.0f;
 
 // One group of 16 tokens as it comes from memory.
 template <int D, int UNI>
@@ -310,7 +315,7 @@ attn_decode_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles)
 #pragma unroll
         for (int h = 0; h < 2; ++h) mx = fmaxf(mx, y[u][2 * h + j]);
       // the first keys of a row, or one far above its reference
-      far = far || mx > mo[j] + 10.f;
+      far = far || mx > mo[j] + kTop;
     }
     if (__any_sync(0xffffffffu, far)) {
 #pragma unroll
@@ -323,6 +328,8 @@ attn_decode_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles)
 #pragma unroll
         for (int sh = 4; sh <= 16; sh <<= 1)
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
+        // another row's keys may have led here: a reference is never lowered
+        mx = fmaxf(mx - kBelow, mo[j]);
         const float keep = ex2(mo[j] - finite(mx));
         l[j] *= keep;
         mo[j] = mx;

@@ -23,10 +23,13 @@
 // scale) and mo a reference of the row, the weight is 2^(y - mo), so the product
 // with the bare codes is the value sum in units of 2^mo whatever the scales are,
 // and l += weight / vs is the softmax sum in the same units: one exponential
-// serves both.  Value scales below 2^-100 count as 2^-100 there.  mo is raised
-// (and O rescaled) only when y passes it by more than 8: weights stay below 2^8,
-// far from fp16's end, and a rescale is rare.  The fp16 rounding of a weight is
-// half a step of 2^-11; scores, sums and O are fp32.
+// serves both.  Value scales below 2^-100 count as 2^-100 there.  Scores, sums and
+// O are fp32; the weights are fp16, the type of the codes they are multiplied with.
+// mo is set 8 below the largest y, and raised (and O rescaled) only when y passes it
+// by more than 15: weights end at 2^15, fp16 at 2^16, and a rescale is rare.  So a
+// weight is off by at most half a step (2^-11 of it) if it is within 2^-22 of the
+// row's largest, and by at most 2^-33 of the largest below that: a long flat tail
+// under one dominating key keeps its sum.
 // Queries are scaled per row by a power of two and exact in fp16, as in
 // attn_decode.cu.  Keys that no row of the CTA sees have zero codes and lg2 vs =
 // -inf, so no stale byte enters a sum.
@@ -66,7 +69,10 @@ constexpr int SN = 64;                  // tokens of a score block
 constexpr int kSoftRegs = 152, kConvRegs = 104;
 constexpr int kSplitRegs = 256 * kSoftRegs + 256 * kConvRegs;
 static_assert(kSplitRegs <= 65536, "register file");
-constexpr float kLazy = 8.0f;           // how far y may pass its reference (log2)
+// The reference of a row is set kBelow (log2) under the largest y, so that the largest
+// weight is 2^8 and those down to 2^-22 of it have all of fp16's bits; y may then pass
+// the reference by 15 before it is raised (fp16 ends at 2^16).
+constexpr float kBelow = 8.0f, kTop = 15.0f;
 
 template <int D>
 struct Lay {
@@ -579,10 +585,10 @@ attn_tc_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles) {
         }
       }
       if constexpr (UNI == SN) mx = fmaf(one.x, mx, one.y);
-      const bool up = mx > mo + kLazy || (mo == -INFINITY && mx != -INFINITY);
+      const bool up = mx > mo + kTop;      // true for the first keys seen
       if (__any_sync(0xffffffffu, up)) {
-        const float f = up ? ex2(mo - mx) : 1.f;     // 0 for the first keys seen
-        if (up) mo = mx;
+        const float f = up ? ex2(mo - (mx - kBelow)) : 1.f;     // 0 for the first keys seen
+        if (up) mo = mx - kBelow;
         l *= f;
         if (i > 0) {
           if (!wait_bar(&o_done[t], (i - 1) & 1, abort_flag, a.status, 0x73Au)) {
