@@ -262,7 +262,7 @@ attn_merge_kernel(const AttnArgs a, const AttnParts p) {
     const float2 x = stat[i];
     if (x.x == 0.f) continue;
     const float f = attn::ex2(x.y - attn::finite(mo));
-    l += x.x * f;
+    l += attn::times_ex2(x.x, x.y - attn::finite(mo));
     const float* o = p.o + (item * p.splits + i) * D;
 #pragma unroll
     for (int e = 0; e < kMaxD / 32; ++e)

@@ -68,8 +68,20 @@ __device__ __forceinline__ float rcp(float x) {
   return y;
 }
 
-// Value scales below this count as it (their values are below 2^-93).
-constexpr float kMinVs = 0x1p-100f;
+// x 2^d for d <= 0, in two steps: the factor alone may be below fp32's smallest where
+// the product is not (sums whose references lie more than 2^126 apart).
+__device__ __forceinline__ float times_ex2(float x, float d) {
+  const float h = ex2(0.5f * d);
+  return x * h * h;
+}
+
+// The value scale as the kernels that fold it into the exponent take it (weight
+// 2^(y - mo) with y = z + lg2 vs, mo within 15 of the row's largest y; the sum's term
+// weight / vs).  A weight leaves fp32 below 2^-126, and its key's term with it: with
+// scales within a factor of 2^100 of one another that is a term below 2^-41 of the sum.
+// Scales below 2^-70, those of zero values among them, count as 2^-70 (their values are
+// below 2^-61), which leaves room for scales up to 2^30.
+__device__ __forceinline__ float value_scale(float vs) { return fmaxf(vs, 0x1p-70f); }
 
 // A running maximum as the reference of a difference: 0 while nothing was seen.
 __device__ __forceinline__ float finite(float m) { return m == -INFINITY ? 0.f : m; }

@@ -270,7 +270,7 @@ attn_decode_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles)
     for (int u = 0; u < NP; ++u)
 #pragma unroll
       for (int h = 0; h < SC; ++h) {
-        const float vs = ok[u] ? fmaxf(G[u * NG / NP].vs[h], kMinVs) : 1.f;
+        const float vs = ok[u] ? value_scale(G[u * NG / NP].vs[h]) : 1.f;
         lv[u][h] = lg2(vs);
         iv[u][h] = rcp(vs);
       }
@@ -331,7 +331,7 @@ attn_decode_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles)
         // another row's keys may have led here: a reference is never lowered
         mx = fmaxf(mx - kBelow, mo[j]);
         const float keep = ex2(mo[j] - finite(mx));
-        l[j] *= keep;
+        l[j] = times_ex2(l[j], mo[j] - finite(mx));
         mo[j] = mx;
 #pragma unroll
         for (int i = 0; i < KS; ++i) {
@@ -412,7 +412,7 @@ attn_decode_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles)
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       const float f = ex2(st[w][row][1] - finite(MO));
-      sum += st[w][row][0] * f;
+      sum += times_ex2(st[w][row][0], st[w][row][1] - finite(MO));
       acc += so[w][row][d] * f;
     }
     const int64_t tok = s.row0 + (R0 + row) / g;

@@ -23,8 +23,7 @@
 // scale) and mo a reference of the row, the weight is 2^(y - mo), so the product
 // with the bare codes is the value sum in units of 2^mo whatever the scales are,
 // and l += weight / vs is the softmax sum in the same units: one exponential
-// serves both.  Value scales below 2^-100 count as 2^-100 there.  Scores, sums and
-// O are fp32; the weights are fp16, the type of the codes they are multiplied with.
+// serves both (value_scale in attn_common.cuh: for which scales).  Scores, sums and O are fp32; the weights are fp16, the type of the codes they are multiplied with.
 // mo is set 8 below the largest y, and raised (and O rescaled) only when y passes it
 // by more than 15: weights end at 2^15, fp16 at 2^16, and a rescale is rare.  So a
 // weight is off by at most half a step (2^-11 of it) if it is within 2^-22 of the
@@ -439,7 +438,7 @@ attn_tc_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles) {
         break;
       if (is_k) {
         float* sc = reinterpret_cast<float*>(smem + L::kSc + (uint32_t)(j & 3) * L::kScSlot);
-        vs = fmaxf(vs, kMinVs);
+        vs = value_scale(vs);
         const float cs = ks * (fabsf(a.scale) * kLog2e);
         const float lv = on ? lg2(vs) : -INFINITY, iv = on ? __fdividef(1.f, vs) : 0.f;
         if constexpr (UNI) {
@@ -587,9 +586,9 @@ attn_tc_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles) {
       if constexpr (UNI == SN) mx = fmaf(one.x, mx, one.y);
       const bool up = mx > mo + kTop;      // true for the first keys seen
       if (__any_sync(0xffffffffu, up)) {
-        const float f = up ? ex2(mo - (mx - kBelow)) : 1.f;     // 0 for the first keys seen
+        const float d = up ? mo - (mx - kBelow) : 0.f, f = ex2(d);   // 0 for the first keys seen
         if (up) mo = mx - kBelow;
-        l *= f;
+        l = times_ex2(l, d);
         if (i > 0) {
           if (!wait_bar(&o_done[t], (i - 1) & 1, abort_flag, a.status, 0x73Au)) {
             ok = false;

@@ -23,7 +23,7 @@ def attention_and_bounds(q, c, off, lens, table, scale):
     2^-33 of the row's largest below fp16's normal range, where a kernel's largest weight is 2^8 or
     more.  A score's error e is that of layer_ref.attention, with 2^-23 of the largest
     exponent (scores, scales and references in log2 units) for exp2 and its argument;
-    sums are fp32.  Value scales below 2^-80 may count as 2^-80."""
+    sums are fp32, in which a key may be lost whose term is below 2^-41 of it."""
     D, H, Hk = q.shape[2], q.shape[1], c.k.shape[1]
     page, bt = c.k.shape[2], c.k.shape[2] // c.ks.shape[2]
     out, lse = torch.zeros(*q.shape, dtype=F8, device="cuda"), torch.zeros(q.shape[:2], dtype=F8, device="cuda")
@@ -44,15 +44,15 @@ def attention_and_bounds(q, c, off, lens, table, scale):
             qq, at = q[o[b]:o[b + 1], h].to(F8), slice(o[b], o[b + 1])
             z = (qq @ (k * ks[:, None]).t() * scale).masked_fill(~seen, -math.inf)
             zmax = z.masked_fill(~seen, 0).abs().amax(1, keepdim=True) / math.log(2)
-            lg = vs.clamp(min=2.0 ** -80).log2().abs().max()
+            lg = vs.clamp(min=2.0 ** -70).log2().abs().max()
             e = ((2 * D + 16) * ref.U32 * abs(scale) * (qq.abs() @ (k.abs() * ks[:, None]).t())).masked_fill(
                 ~seen, 0).amax(1, keepdim=True) + (2 * zmax + 2 * lg + 64) * 2.0 ** -23
             p = torch.softmax(z, 1)
-            w, small = p * vs, p * torch.where(vs < 2.0 ** -80, 2.0 ** -80, 0.0)
+            w = p * vs
             out[at, h] = w @ v
             lse[at, h] = torch.logsumexp(z, 1)
             tol[at, h] = (ref.UBF16 * out[at, h].abs() + (2 * e + ref.UFP16 + 2 * len_ * ref.U32) *
-                          (w @ v.abs()) + small @ v.abs() +
+                          (w @ v.abs()) +
                           2.0 ** -33 * w.amax(1, keepdim=True) * (seen.to(F8) @ v.abs()))
             ltol[at, h] = (e + 8 * ref.U32 * (zmax + lg + 64))[:, 0] + 2 * len_ * ref.U32
     return out, lse, tol, ltol
@@ -100,3 +100,64 @@ def test_a_tail_under_dominating_keys_keeps_its_sum(L, case, gap, dtype):    # n
     q = randn(g, sum(new), Hq, D).bfloat16()
     q[..., 0] = 1
     check(q, c, off, ln, table, gap * math.log(2))
+
+
+def draw_scales(g, s, how):
+    """Value scales [pages, heads, blocks] for one of the ways that they can differ."""
+    u = torch.rand(s.shape, generator=g, device="cuda")
+    some = torch.rand(s.shape, generator=g, device="cuda") < 0.4
+    if how == "zeros":                      # blocks of zeros between ordinary ones
+        return torch.where(some, 0.0, 0.01 + u)
+    if how == "zeros beside huge":
+        return torch.where(some, 0.0, (1 + u) * 2.0 ** 29)
+    if how == "outliers":                   # a few blocks far above the others
+        return torch.where(u < 0.1, 2.0 ** 20, 0.01)
+    if how == "spread":                     # all that the sum is promised for
+        return torch.exp2(100 * u - 70)
+    if how == "tiny":
+        return torch.exp2(-60 - 10 * u)
+    assert how == "none"                    # every value is zero
+    return torch.zeros_like(u)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [bq.INT8, bq.FP8_E4M3])
+@pytest.mark.parametrize("how", ["zeros", "zeros beside huge", "outliers", "spread", "tiny", "none"])
+@pytest.mark.parametrize("case", KERNELS, ids=IDS)
+def test_attention_with_scales_far_apart(L, case, how, dtype):               # noqa: F811
+    """Blocks of zero keys and of zero values, which are written with a scale of zero, and
+    value scales over many powers of two: out and lse."""
+    new, lens, Hq, Hk, D, page, bt = case
+    g = gen(3 * D + bt)
+    off, ln, table, count = make_batch(g, new, lens, page)
+    c = random_cache(g, count, Hk, page, D, bt, dtype)
+    c.vs.copy_(draw_scales(g, c.vs, how))
+    c.ks.mul_(torch.rand(c.ks.shape, generator=g, device="cuda") > 0.3)
+    for b, n in enumerate(lens):            # the first and the last block of each sequence
+        for t in (0, n - 1):
+            c.vs[int(table[b, t // page]), :, t % page // bt] = 0 if how != "tiny" else 2.0 ** -65
+    for codes, s in ((c.k, c.ks), (c.v, c.vs)):
+        codes.mul_((s != 0).repeat_interleave(bt, 2)[..., None])
+    q = randn(g, sum(new), Hq, D).bfloat16()
+    check(q, c, off, ln, table, 1 / math.sqrt(D))
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [bq.INT8, bq.FP8_E4M3])
+@pytest.mark.parametrize("order", ["huge last", "huge first"])
+@pytest.mark.parametrize("case", KERNELS, ids=IDS)
+def test_keys_of_zero_value_stay_in_the_sum_beside_huge_ones(L, case, order, dtype):    # noqa: F811
+    """Half of the sequence has values of zero, the other half scales of 2^30: references
+    that lie 2^100 apart in one kernel, and in the parts that are joined."""
+    new, lens, Hq, Hk, D, page, bt = case
+    g = gen(5 * D + bt)
+    off, ln, table, count = make_batch(g, new, lens, page)
+    c = random_cache(g, count, Hk, page, D, bt, dtype)
+    c.vs.zero_()
+    for b, n in enumerate(lens):
+        for t in range(0, n, bt):
+            if (t < n // 2) == (order == "huge first"):
+                c.vs[int(table[b, t // page]), :, t % page // bt] = 2.0 ** 30
+    c.v.mul_((c.vs != 0).repeat_interleave(bt, 2)[..., None])
+    q = randn(g, sum(new), Hq, D).bfloat16()
+    check(q, c, off, ln, table, 1 / math.sqrt(D))
