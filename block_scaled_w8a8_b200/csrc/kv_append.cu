@@ -126,18 +126,19 @@ __global__ void __launch_bounds__(kAnyThreads) append_any_kernel(const AppendArg
 }
 
 // pack4_codes of v for a scale s in [2^-80, inf) with rs = 1 / s correctly
-// rounded, without four divisions: q = v rs, its remainder v - q s (exact in one
-// FMA), q + remainder * rs, is the correctly rounded quotient (Markstein,
+// rounded, without four divisions: q = v rs, its remainder q s - v (exact in one
+// FMA), q - remainder * rs, is the correctly rounded quotient (Markstein,
 // "Computation of elementary functions on the IBM RISC System/6000 processor",
 // 1990), as long as the remainder does not underflow: a code other than zero
-// needs |v| > s 2^-11, far above that for such s.
+// needs |v| > s 2^-11, far above that for such s.  The remainder's sign is taken so
+// that a zero keeps its own: -0 gives -0 - (+0), where v - q s would give -0 + (+0).
 template <int DT>
 __device__ __forceinline__ uint32_t pack4_recip(const float v[4], float s, float rs) {
   float q[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float q0 = v[i] * rs;
-    q[i] = fmaf(fmaf(-q0, s, v[i]), rs, q0);
+    q[i] = fmaf(-fmaf(q0, s, -v[i]), rs, q0);
   }
   if (DT == kInt8) {
     uint32_t b[4];               // round to nearest even; the code in the low byte

@@ -161,3 +161,38 @@ def test_keys_of_zero_value_stay_in_the_sum_beside_huge_ones(L, case, order, dty
     c.v.mul_((c.vs != 0).repeat_interleave(bt, 2)[..., None])
     q = randn(g, sum(new), Hq, D).bfloat16()
     check(q, c, off, ln, table, 1 / math.sqrt(D))
+
+
+# ---- cache -------------------------------------------------------------------------
+
+def one_append(k, v, H, D, page, bt, dtype):
+    """The cache after one call with all of k, v as a sequence, and what the definition says."""
+    T = k.shape[0]
+    pages = -(-T // page)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    off, lens = torch.tensor([0, T], **i32), torch.tensor([T], **i32)
+    table = torch.arange(pages, **i32).view(1, pages)
+    c = bq.kv_cache(pages, H, page, D, bt, dtype)
+    want = [ref.append(a, s, x, off, lens, table, dtype) for a, s, x in ((c.k, c.ks, k), (c.v, c.vs, v))]
+    bq.kv_append(c, k, v, off, lens, table)
+    bq.check_device_status()
+    return c, want
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [bq.INT8, bq.FP8_E4M3])
+@pytest.mark.parametrize("H,D,page,bt", [(2, 128, 32, 16), (1, 64, 16, 1), (2, 8, 8, 4), (1, 5, 8, 4),
+                                         (1, 256, 128, 128)])
+def test_append_keeps_the_sign_of_zero(L, H, D, page, bt, dtype):            # noqa: F811
+    """-0, and negative values whose code is a zero, byte for byte."""
+    g = gen(D + bt)
+    k, v = (randn(g, 3 * page - 1, H, D).bfloat16() for _ in range(2))
+    for x in (k, v):
+        kind = torch.randint(0, 4, x.shape, generator=g, device="cuda")
+        x.copy_(torch.where(kind == 0, -0.0, torch.where(kind == 1, x * 2.0 ** -24, x)))
+        x[1].fill_(-0.0)
+    c, want = one_append(k, v, H, D, page, bt, dtype)
+    for got, scales, (codes, s) in ((c.k, c.ks, want[0]), (c.v, c.vs, want[1])):
+        assert torch.equal(got, codes) and torch.equal(scales, s)
+    if dtype == bq.FP8_E4M3:
+        assert (c.k == 0x80).any() and (c.k == 0).any()
