@@ -105,6 +105,19 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
+// The larger of two; NaN if either is one (fmaxf gives the other).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
+
+__device__ __forceinline__ float warp_max_nan(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
 __device__ __forceinline__ float bf16_bits_to_float(uint16_t h) {
   return __uint_as_float(((uint32_t)h) << 16);
 }

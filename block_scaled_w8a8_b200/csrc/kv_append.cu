@@ -8,7 +8,9 @@
 // code() and the division are those of the activation quantiser (IEEE fp32,
 // round to nearest even).  A block whose new tokens fit the old scale keeps its
 // old codes, so writing the same tokens again changes nothing.  Slots behind
-// the last token keep what they hold.
+// the last token keep what they hold.  Both maxima carry a NaN on: a block with one
+// has a NaN scale, until its first token is written anew, instead of finite codes
+// for a scale that left the NaN out.
 #include <algorithm>
 
 #include "bq_common.cuh"
@@ -108,13 +110,13 @@ __global__ void __launch_bounds__(kAnyThreads) append_any_kernel(const AppendArg
   const int n_old = w.t0 - w.tb, n_new = w.t1 - w.t0;
   float amax = 0.f;
   for (int e = tid; e < n_new * D; e += kAnyThreads)
-    amax = fmaxf(amax, fabsf(bf16_bits_to_float(x[(e / D) * ld + e % D])));
-  amax = warp_max(amax);
+    amax = max_nan(amax, fabsf(bf16_bits_to_float(x[(e / D) * ld + e % D])));
+  amax = warp_max_nan(amax);
   if ((tid & 31) == 0) red[tid >> 5] = amax;
   const float s_old = n_old > 0 ? *scale : 0.f;
   __syncthreads();
-  amax = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-  const float s_new = fmaxf(s_old, group_scale<DT>(amax));
+  amax = max_nan(max_nan(red[0], red[1]), max_nan(red[2], red[3]));
+  const float s_new = max_nan(s_old, group_scale<DT>(amax));
   for (int e = tid; e < n_new * D; e += kAnyThreads)
     codes[n_old * D + e] = one_code<DT>(bf16_bits_to_float(x[(e / D) * ld + e % D]), s_new);
   if (s_new > s_old) {
@@ -165,7 +167,7 @@ constexpr int kVecThreads = 512;
 template <int DT>
 __global__ void __launch_bounds__(kVecThreads, 1)
 append_vec_kernel(const AppendArgs a, const int NW) {
-  __shared__ float red[2][kVecThreads / 32];
+  __shared__ uint32_t red[2][kVecThreads / 32];
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -201,35 +203,36 @@ append_vec_kernel(const AppendArgs a, const int NW) {
   const int in_page = w.tb % a.c.page;
   const int64_t code0 = (ph * a.c.page + in_page) * D;          // of token tb
   const int64_t blk = ph * (a.c.page / a.c.bt) + in_page / a.c.bt;
-  float s_old[2] = {0.f, 0.f}, amax[2];
+  float s_old[2] = {0.f, 0.f};
+  uint32_t amax[2];
   if (n_old > 0) {
     s_old[0] = a.c.ks[blk];
     s_old[1] = a.c.vs[blk];
   }
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
-    // magnitudes of bf16 compare as whole numbers, two at a time
+    // magnitudes compare as whole numbers, bf16 two at a time; a NaN's is the largest
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
       top = __vimax3_u16x2(top, v[c][i].x & 0x7FFF7FFFu, v[c][i].y & 0x7FFF7FFFu);
       top = __vimax3_u16x2(top, v[c][i].z & 0x7FFF7FFFu, v[c][i].w & 0x7FFF7FFFu);
     }
-    amax[c] = warp_max(fmaxf(__uint_as_float(top << 16), __uint_as_float(top & 0xFFFF0000u)));
+    amax[c] = __reduce_max_sync(0xffffffffu, max(top << 16, top & 0xFFFF0000u));
     if (NW > 1 && lane == 0) red[c][warp] = amax[c];
   }
   if (NW > 1) {
     asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(nt) : "memory");
-    amax[0] = amax[1] = 0.f;
+    amax[0] = amax[1] = 0;
     for (int i = 0; i < NW; ++i) {
-      amax[0] = fmaxf(amax[0], red[0][group * NW + i]);
-      amax[1] = fmaxf(amax[1], red[1][group * NW + i]);
+      amax[0] = max(amax[0], red[0][group * NW + i]);
+      amax[1] = max(amax[1], red[1][group * NW + i]);
     }
   }
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     uint8_t* codes = (c ? a.c.v : a.c.k) + code0;
-    const float s_new = fmaxf(s_old[c], group_scale<DT>(amax[c]));
+    const float s_new = max_nan(s_old[c], group_scale<DT>(__uint_as_float(amax[c])));
     const bool fast = s_new >= 0x1p-80f && s_new < INFINITY;
     const float rs = fast ? __fdiv_rn(1.0f, s_new) : 0.f;
 #pragma unroll

@@ -574,6 +574,8 @@ bq_status bq_rope(const void* x, int64_t ldt, int64_t ldh, const int32_t* positi
  *   s' = max(s_old, amax(new) / Q), s_old = 0 if n_old == 0;
  *   new codes as bq_quant_act with scale s';
  *   if s' > s_old, the n_old old codes become the codes of (q_old * s_old).
+ * A block that is given a NaN has a NaN scale until its first token is written anew
+ * (its new codes: 0 INT8, 0x7F FP8); other blocks are not touched by it.
  * Slots behind the last token keep their bytes.  A sequence must hold its new
  * tokens (kv_lens[b] >= their number).  A page that a call writes belongs to
  * one sequence of that call.  Writing the same tokens again changes nothing. */

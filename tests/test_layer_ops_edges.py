@@ -196,3 +196,50 @@ def test_append_keeps_the_sign_of_zero(L, H, D, page, bt, dtype):            # n
         assert torch.equal(got, codes) and torch.equal(scales, s)
     if dtype == bq.FP8_E4M3:
         assert (c.k == 0x80).any() and (c.k == 0).any()
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [bq.INT8, bq.FP8_E4M3])
+@pytest.mark.parametrize("H,D,page,bt", [(2, 128, 32, 16), (1, 64, 16, 1), (3, 8, 32, 32), (1, 256, 128, 128)])
+def test_append_with_values_that_are_not_numbers(L, H, D, page, bt, dtype):  # noqa: F811
+    """A block with a NaN has a NaN scale, at any alignment; all others are what they are
+    without it, and the next sequence to use the block finds nothing of it."""
+    g = gen(7 * D + bt)
+    T = 4 * page - 3
+    k, v = (randn(g, T, H, D).bfloat16() for _ in range(2))
+    k[0, 0, D // 2] = 3.0
+    k[0, 0, 1], v[page + 1, H - 1, D - 1], v[2 * page, 0] = math.nan, -math.nan, math.nan
+    _, want = one_append(k.nan_to_num(0.0), v.nan_to_num(0.0), H, D, page, bt, dtype)
+    pages = want[0][0].shape[0]
+
+    def shifted(x):                         # an address that no vector load takes
+        return torch.empty(x.numel() + 1, dtype=x.dtype, device="cuda")[1:].view(x.shape).copy_(x)
+
+    def per_block(x):
+        full = torch.zeros(pages * page, H, D, dtype=x.dtype, device="cuda")
+        full[:T] = x
+        return full.view(pages, page // bt, bt, H, D).permute(0, 3, 1, 2, 4).flatten(3).any(3)
+
+    code = 0 if dtype == bq.INT8 else 0x7F
+    live = per_block(torch.ones_like(k, dtype=torch.bool))
+    for kk, vv in ((k, v), (shifted(k), shifted(v))):
+        c, _ = one_append(kk, vv, H, D, page, bt, dtype)
+        for x, got, s, (codes, scales) in ((k, c.k, c.ks, want[0]), (v, c.v, c.vs, want[1])):
+            bad = per_block(x.isnan())
+            assert bad.any() and not bad[live].all()
+            assert s[bad].isnan().all() and torch.equal(s[~bad], scales[~bad])
+            wide = bad.repeat_interleave(bt, 2)
+            assert torch.equal(got[~wide], codes[~wide])
+            written = torch.zeros(pages * page, dtype=torch.bool, device="cuda")
+            written[:T] = True
+            assert (got[wide & written.view(pages, 1, page)] == code).all()
+        # a token more does not make the block a number again; its first one does
+        i32 = dict(dtype=torch.int32, device="cuda")
+        table = torch.arange(pages, **i32).view(1, pages)
+        one = torch.ones(1, H, D, dtype=torch.bfloat16, device="cuda")
+        if bt > 1:
+            bq.kv_append(c, one, one, torch.tensor([0, 1], **i32), torch.tensor([2], **i32), table)
+            assert c.ks[0, 0, 0].isnan() and c.vs[0, 0, 0] == c.vs[0, 0, 0]
+        bq.kv_append(c, one, one, torch.tensor([0, 1], **i32), torch.tensor([1], **i32), table)
+        assert (c.ks[0, :, 0] == 1 / torch.full((1,), ref.QMAX[dtype], device="cuda")).all()
+    bq.check_device_status()
