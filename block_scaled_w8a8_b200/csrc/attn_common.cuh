@@ -80,8 +80,8 @@ __device__ __forceinline__ float times_ex2(float x, float d) {
 // weight / vs).  A weight leaves fp32 below 2^-126, and its key's term with it: with
 // scales within a factor of 2^100 of one another that is a term below 2^-41 of the sum.
 // Scales below 2^-70, those of zero values among them, count as 2^-70 (their values are
-// below 2^-61), which leaves room for scales up to 2^30.
-__device__ __forceinline__ float value_scale(float vs) { return fmaxf(vs, 0x1p-70f); }
+// below 2^-61), which leaves room for scales up to 2^30.  A NaN stays one.
+__device__ __forceinline__ float value_scale(float vs) { return max_nan(vs, 0x1p-70f); }
 
 // A running maximum as the reference of a difference: 0 while nothing was seen.
 __device__ __forceinline__ float finite(float m) { return m == -INFINITY ? 0.f : m; }

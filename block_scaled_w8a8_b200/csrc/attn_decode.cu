@@ -303,6 +303,14 @@ attn_decode_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles)
             if (!ok[u * NP / NG] || tok < lo || tok >= hi) y[u][2 * h + j] = -INFINITY;
           }
       }
+      // scales that belong to no key in sight may be anything, NaN among it
+#pragma unroll
+      for (int u = 0; u < NP; ++u)
+#pragma unroll
+        for (int h = 0; h < SC; ++h) {
+          const int tok = t + TP * u + (UNI ? TP - 1 : r + 8 * h);
+          if (tok < all.lo || (!UNI && tok >= part.hi)) iv[u][h] = 0.f;
+        }
     }
     // weights
     uint32_t pf[NG][2];

@@ -192,18 +192,19 @@ __device__ __forceinline__ void ld_shared4(const float4* p, float (&v)[4]) {
 
 // Scales of a group of 16 tokens: y = c s + lv for a score product s of a row
 // with power rd, and 1 / vs.  c is kept above zero, so that a masked score of
-// -inf stays one (codes under a zero scale are zero, and so are their products).
+// -inf stays one (codes under a zero scale are zero, and so are their products); a
+// NaN stays one too.
 __device__ __forceinline__ void group_scales(const float4* sc, float rd, float& c, float& lv,
                                              float& iv) {
   const float4 x = *sc;
-  c = fmaxf(x.x * rd, 1e-37f);
+  c = max_nan(x.x * rd, 1e-37f);
   lv = x.y;
   iv = x.z;
 }
 
 // y of one token (own scales): c = cs, lv = lg2 vs.
 __device__ __forceinline__ float token_y(uint32_t s, float cs, float rd, float lv) {
-  return fmaf(__uint_as_float(s), fmaxf(cs * rd, 1e-37f), lv);
+  return fmaf(__uint_as_float(s), max_nan(cs * rd, 1e-37f), lv);
 }
 
 __device__ __forceinline__ void fence_async_shared() {

@@ -604,8 +604,9 @@ bq_status bq_kv_attention_workspace_size(int64_t B, int64_t T, int64_t Hq, int64
  * row that sees no key gives zeros and lse = -inf.
  * Slots of a page behind kv_lens[b] may hold any bytes, and pages that hold only
  * keys in front of every row's window need not exist (any number in the table).
- * The keys and values that some row of the call sees, and the queries, must be
- * finite.
+ * The keys and values that some row of a sequence sees, and its queries, must be
+ * finite; a NaN among them (a scale that bq_kv_append made NaN) makes the rows that
+ * see it NaN, and may do so to other rows of that sequence in the call.
  * q: bf16, element (t, h, d) at q[t * ldq + h * hq + d]; out likewise with ldo,
  * ho (no overlap with q); lse: fp32 [T][Hq] or NULL.  max_q_len and max_kv_len
  * bound every sequence's rows and length (a longer sequence is skipped and

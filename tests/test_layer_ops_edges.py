@@ -243,3 +243,31 @@ def test_append_with_values_that_are_not_numbers(L, H, D, page, bt, dtype):  # n
         bq.kv_append(c, one, one, torch.tensor([0, 1], **i32), torch.tensor([1], **i32), table)
         assert (c.ks[0, :, 0] == 1 / torch.full((1,), ref.QMAX[dtype], device="cuda")).all()
     bq.check_device_status()
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [bq.INT8, bq.FP8_E4M3])
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("case", KERNELS, ids=IDS)
+def test_attention_shows_values_that_are_not_numbers(L, case, which, dtype):  # noqa: F811
+    """A block with a NaN scale makes the rows that see it NaN, and no other sequence."""
+    new, lens, Hq, Hk, D, page, bt = case
+    new, lens = new[:1] + [3], lens[:1] + [900]
+    g = gen(11 * D + bt)
+    off, ln, table, count = make_batch(g, new, lens, page)
+    c = random_cache(g, count, Hk, page, D, bt, dtype)
+    q = randn(g, sum(new), Hq, D).bfloat16()
+    clean = bq.kv_attention(q, c, off, ln, table, max(new), max(lens))
+    for t in (5, lens[0] // 2, lens[0] - new[0]):          # all rows of the first sequence see them
+        s = (c.ks if which == "k" else c.vs)[int(table[0, t // page]), Hk - 1, t % page // bt:][:1]
+        kept = s.clone()
+        s.fill_(math.nan)
+        lse = torch.zeros(sum(new), Hq, device="cuda")
+        got = bq.kv_attention(q, c, off, ln, table, max(new), max(lens), lse=lse)
+        s.copy_(kept)
+        heads = torch.arange(Hq, device="cuda") // (Hq // Hk) == Hk - 1
+        assert got[:new[0], heads].isnan().all()
+        assert which == "v" or lse[:new[0], heads].isnan().all()
+        assert torch.equal(got[:, ~heads], clean[:, ~heads])
+        assert torch.equal(got[new[0]:], clean[new[0]:])
+    bq.check_device_status()
