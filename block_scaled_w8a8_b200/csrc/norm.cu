@@ -8,6 +8,8 @@
 // the stored residual and the normalised row agree.  The codes come from the
 // fp32 y: the bf16 rounding between a separate norm and quantiser is left out.
 // The sum of squares is fp32 (a product of two bf16 is exact in it).
+// INT8, FP8: a group with a y that is not a number has a scale that is not one.  MXFP8:
+// the codes are e4m3's NaN, and the scale is that of the other values.
 #include <algorithm>
 
 #include "bq_common.cuh"
@@ -94,6 +96,12 @@ __device__ __forceinline__ float inv_sqrt(float x) {
   return fmaf(0.5f * r, e, r);
 }
 
+// The running largest magnitude of a group, as the type's scale wants it.
+template <int DT>
+__device__ __forceinline__ float largest(float amax, float v) {
+  return DT == kMxFp8 ? fmaxf(amax, fabsf(v)) : max_nan(amax, fabsf(v));
+}
+
 // Four codes of y * inv, |y * inv| <= 127 (1 + 2^-22): round to nearest even.
 __device__ __forceinline__ uint32_t int8x4(const float* y, float inv) {
   uint32_t b[4];
@@ -141,9 +149,9 @@ __global__ void __launch_bounds__(kAnyThreads) norm_any_kernel(const NormArgs a)
       const int64_t k0 = g * a.group, k1 = min(k0 + a.group, a.K);
       float amax = 0.f;
       for (int64_t k = k0 + lane; k < k1; k += 32)
-        amax = fmaxf(amax, fabsf(bf16_bits_to_float(row[k]) *
-                                 (bf16_bits_to_float(a.w[k]) + a.w_off) * rstd));
-      amax = warp_max(amax);
+        amax = largest<DT>(amax, bf16_bits_to_float(row[k]) *
+                                     (bf16_bits_to_float(a.w[k]) + a.w_off) * rstd);
+      amax = warp_max_nan(amax);
       float sc = 0.f, inv = 0.f;
       if (DT == kMxFp8) {
         const int se = mx_exponent(amax);
@@ -250,12 +258,12 @@ norm_vec_kernel(const NormArgs a, const int lpg) {       // lpg: lanes of a grou
         float t[8];
         weighted(rv[i], wv[i], a.w_off, t);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) row_max = fmaxf(row_max, fabsf(t[e]));
+        for (int e = 0; e < 8; ++e) row_max = largest<DT>(row_max, t[e]);
       }
-      row_max = warp_max(row_max);
+      row_max = warp_max_nan(row_max);
       if (lane == 0) red[parity][1][warp] = row_max;
       __syncthreads();
-      row_max = warp_max(lane < nw ? red[parity][1][lane] : 0.f);
+      row_max = warp_max_nan(lane < nw ? red[parity][1][lane] : 0.f);
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -264,17 +272,17 @@ norm_vec_kernel(const NormArgs a, const int lpg) {       // lpg: lanes of a grou
       weighted(rv[i], wv[i], a.w_off, t);
       float amax = 0.f;                        // of t
 #pragma unroll
-      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(t[e]));
+      for (int e = 0; e < 8; ++e) amax = largest<DT>(amax, t[e]);
 #pragma unroll
       for (int o = 16; o >= 1; o >>= 1)
-        if (o < lpg) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        if (o < lpg) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       if (lpg == 0) amax = row_max;
       if (v >= nvec) continue;                 // no shuffle below
       const bool first = lpg == 0 ? v == 0 : (v & (lpg - 1)) == 0;
       const int64_t g = lpg == 0 ? 0 : v / lpg;
       uint2 q;
       if (DT == kMxFp8) {
-        const int se = mx_exponent(amax * rstd);
+        const int se = mx_exponent(fmaxf(amax * rstd, 0.f));     // 0 for a row that is all NaN
         const float inv = __uint_as_float((uint32_t)(127 - se) << 23);   // 2^-se, exact
         float y[8];
 #pragma unroll
@@ -286,7 +294,8 @@ norm_vec_kernel(const NormArgs a, const int lpg) {       // lpg: lanes of a grou
         constexpr float kQ = DT == kInt8 ? 127.0f : 448.0f;
         const float top = amax * rstd;
         float sc;
-        if (fminf(amax, top) >= 0x1p-100f && fmaxf(amax, top) <= 0x1p100f) {
+        // a NaN fails, which may be in either
+        if (amax >= 0x1p-100f && top >= 0x1p-100f && amax <= 0x1p100f && top <= 0x1p100f) {
           sc = quotient(top, kQ, 1.0f / kQ);
           const float f = quotient(kQ, amax, rcp(amax));
           q.x = DT == kInt8 ? int8x4(t, f) : e4m3x4(t, f);

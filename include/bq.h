@@ -491,7 +491,8 @@ bq_status bq_moe_combine(const void* y, int64_t ldy, const int32_t* inv_perm,
  * would round it to bf16 in between).  x: bf16 [M, K] (row stride ldx >= K);
  * residual: bf16 [M, K] (row stride ldr) or NULL; weight: bf16 [K];
  * weight_offset: 0, or 1 for weights stored as their difference from 1.
- * q: codes [M, K] (row stride ldq), s: fp32 [ceil(K/group_k)][M].
+ * q: codes [M, K] (row stride ldq), s: fp32 [ceil(K/group_k)][M]; a group with a y
+ * that is not a number has a NaN scale.
  * res_out: r as bf16 [M, K] (row stride ldro), or NULL; it may be residual or
  * x itself (same pointer and stride).  h_out: y rounded to bf16 [M, K] (row
  * stride ldh), or NULL.  Other overlaps of inputs and outputs are not allowed.
@@ -503,7 +504,8 @@ bq_status bq_rmsnorm_quant(const void* x, int64_t ldx, const void* residual, int
 
 /* The same norm with the MXFP8 quantisation of y (rule and scale layout of
  * bq_mx_quant_act): q e4m3 [M, K] (row stride ldq, 4-byte aligned rows), sf
- * the scale array (bq_mx_scale_bytes(M, K) bytes).  K a multiple of 128. */
+ * the scale array (bq_mx_scale_bytes(M, K) bytes); a y that is not a number has
+ * e4m3's NaN as its code.  K a multiple of 128. */
 bq_status bq_mx_rmsnorm_quant(const void* x, int64_t ldx, const void* residual, int64_t ldr,
                               const void* weight, float weight_offset, float eps, int64_t M,
                               int64_t K, void* q, int64_t ldq, void* sf, void* res_out,

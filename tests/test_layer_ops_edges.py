@@ -271,3 +271,59 @@ def test_attention_shows_values_that_are_not_numbers(L, case, which, dtype):  # 
         assert torch.equal(got[:, ~heads], clean[:, ~heads])
         assert torch.equal(got[new[0]:], clean[new[0]:])
     bq.check_device_status()
+
+
+# ---- norm --------------------------------------------------------------------------
+
+def shifted(x):
+    """A copy at an address, and with a row stride, that no vector load takes."""
+    M, K = x.shape
+    return torch.zeros(M, K + 3, dtype=x.dtype, device="cuda")[:, 1:1 + K].copy_(x)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [bq.INT8, bq.FP8_E4M3])
+@pytest.mark.parametrize("K,group", [(1024, 128), (512, 512), (256, 8)])
+def test_norm_with_values_that_are_not_numbers(L, K, group, dtype):          # noqa: F811
+    """A NaN makes its row NaN, an infinity its group (the other values are divided by
+    infinity), a NaN weight its column's group: in the scales, at any alignment."""
+    g = gen(K + group)
+    x, w = randn(g, 6, K).bfloat16(), (1 + 0.2 * randn(g, K)).bfloat16()
+    clean_q, clean_s = bq.rmsnorm_quant(x, w, group_k=group, dtype=dtype)
+    x[1, K - 3], x[2, 5], x[4, K // 2] = math.nan, math.inf, -math.nan
+    wn = w.clone()
+    wn[K // 2 + 1] = math.nan
+    code = 0 if dtype == bq.INT8 else 0x7F
+    at = K // 2 // group                    # the group of column K // 2, and of the next one
+    for view in (x, shifted(x)):
+        q, s = bq.rmsnorm_quant(view, w, group_k=group, dtype=dtype)
+        for m in (1, 4):
+            assert s[:, m].isnan().all() and (q[m] == code).all()
+        assert s[0, 2].isnan() and (s[1:, 2] == 0).all() and (q[2, group:] == 0).all()
+        c, n = bq.rmsnorm_quant(view, wn, group_k=group, dtype=dtype)
+        for m in (0, 3, 5):
+            if view is x:
+                assert torch.equal(q[m], clean_q[m]) and torch.equal(s[:, m], clean_s[:, m])
+            assert n[at, m].isnan() and not n[:at, m].isnan().any() and not n[at + 1:, m].isnan().any()
+            keep = torch.arange(K, device="cuda") // group != at
+            assert torch.equal(c[m, keep], q[m, keep])
+            assert (c[m, ~keep] == code).all()
+
+
+@gpu
+def test_mx_norm_with_values_that_are_not_numbers(L):                        # noqa: F811
+    import gpu_util
+    K, g = 256, gen(41)
+    x, w = randn(g, 5, K).bfloat16(), (1 + 0.2 * randn(g, K)).bfloat16()
+    x[1, 7] = math.nan
+    w[40] = math.nan
+    got = []
+    for view in (x, shifted(x)):
+        q, sf = bq.mx_rmsnorm_quant(view, w)
+        e = gpu_util.mx_sf_rows(sf, 5, K)
+        assert (q[1] == 0x7F).all() and (e[1] == 0).all()
+        assert (q[:, 40] & 0x7F == 0x7F).all()
+        rest = torch.arange(K, device="cuda") != 40
+        assert not (q[[0, 2, 3, 4]][:, rest] & 0x7F == 0x7F).any()
+        got.append((q, torch.from_numpy(e)))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
