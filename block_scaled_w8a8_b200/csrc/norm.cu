@@ -117,6 +117,26 @@ __device__ __forceinline__ uint32_t e4m3x4(const float* y, float inv) {
   return (uint32_t)lo | (uint32_t)hi << 16;
 }
 
+// Scale of an INT8 or FP8 group and the factor of its codes from amax = max |t|, where
+// y = t rstd and t = r (w + w_off): rstd falls out of y / s, so the codes are those of
+// t Q / max |t|, in which only Q / max |t| and the product round, and the scale is
+// max |t| rstd / Q.  Both kernels go by it, so that codes do not depend on the order
+// of a row's sum, nor on strides and alignment.  False where the factor may not be a
+// number; the codes are then those of y / s, divided.
+template <int DT>
+__device__ __forceinline__ bool group_factor(float amax, float rstd, float& sc, float& f) {
+  constexpr float kQ = DT == kInt8 ? 127.0f : 448.0f;
+  const float top = amax * rstd;
+  // a NaN fails, which may be in either
+  if (amax >= 0x1p-100f && top >= 0x1p-100f && amax <= 0x1p100f && top <= 0x1p100f) {
+    sc = quotient(top, kQ, 1.0f / kQ);
+    f = quotient(kQ, amax, rcp(amax));
+    return true;
+  }
+  sc = group_scale<DT>(top);
+  return false;
+}
+
 // Any width, group, stride and alignment: a CTA per row, the row's r in shared
 // memory as bf16 (exactly what res_out holds), a warp per group.
 template <int DT>
@@ -150,24 +170,27 @@ __global__ void __launch_bounds__(kAnyThreads) norm_any_kernel(const NormArgs a)
       float amax = 0.f;
       for (int64_t k = k0 + lane; k < k1; k += 32)
         amax = largest<DT>(amax, bf16_bits_to_float(row[k]) *
-                                     (bf16_bits_to_float(a.w[k]) + a.w_off) * rstd);
-      amax = warp_max_nan(amax);
+                                     (bf16_bits_to_float(a.w[k]) + a.w_off));
+      amax = warp_max_nan(amax);                                   // of t, y = t rstd
       float sc = 0.f, inv = 0.f;
+      bool fast = false;
       if (DT == kMxFp8) {
-        const int se = mx_exponent(amax);
+        const int se = mx_exponent(fmaxf(amax * rstd, 0.f));       // 0 for a row that is all NaN
         inv = __uint_as_float((uint32_t)(127 - se) << 23);   // 2^-se, exact
         if (lane == 0) a.sf[mx_sf_index(m, g, a.K)] = (uint8_t)(se + 127);
       } else {
-        sc = group_scale<DT>(amax);
+        fast = group_factor<DT>(amax, rstd, sc, inv);
         if (lane == 0) a.s[g * a.M + m] = sc;
       }
       for (int64_t k = k0 + lane; k < k1; k += 32) {
-        const float y = bf16_bits_to_float(row[k]) *
-                        (bf16_bits_to_float(a.w[k]) + a.w_off) * rstd;
+        const float t = bf16_bits_to_float(row[k]) * (bf16_bits_to_float(a.w[k]) + a.w_off);
+        const float y = t * rstd;
         if (DT == kMxFp8)
           a.q[m * a.ldq + k] = (uint8_t)(e4m3x2_code(y * inv, 0.f, 1.0f) & 0xFFu);
+        else if (DT == kInt8 && fast)
+          a.q[m * a.ldq + k] = (uint8_t)__float_as_uint(fmaf(t, inv, 12582912.0f));
         else
-          a.q[m * a.ldq + k] = one_code<DT>(y, sc);
+          a.q[m * a.ldq + k] = fast ? one_code<DT>(t * inv, 1.0f) : one_code<DT>(y, sc);
         if (a.h) a.h[m * a.ldh + k] = float_to_bf16_bits(y);
       }
     }
@@ -183,11 +206,8 @@ __global__ void __launch_bounds__(kAnyThreads) norm_any_kernel(const NormArgs a)
 // 5.0 TB/s; 2047 x 14336 to MXFP8: 36.1 us, 5.7 TB/s: what it issues (three quarters
 // of the issue slots) stands in the way of the rest.  In place is safe: a row is loaded
 // and stored by one CTA, each element by one thread, loads first.
-//
-// y = t rstd with t = r (w + w_off), and rstd falls out of y / s: the codes are those
-// of t Q / max |t|, where only Q / max |t| and the product round, and the scale is
-// max |t| rstd / Q.  INT8: fma(t, Q / max |t|, 1.5 * 2^23) rounds to nearest even
-// and leaves the code in the low byte, with no conversion unit involved.
+// INT8: fma(t, Q / max |t|, 1.5 * 2^23) rounds to nearest even and leaves the code in
+// the low byte, with no conversion unit involved.
 template <int DT, int V>
 __global__ void __launch_bounds__(V <= 2 ? 1024 : 512)
 norm_vec_kernel(const NormArgs a, const int lpg) {       // lpg: lanes of a group, 0 = the row
@@ -291,17 +311,11 @@ norm_vec_kernel(const NormArgs a, const int lpg) {       // lpg: lanes of a grou
         q.y = e4m3x4(y + 4, inv);
         if (first) a.sf[mx_sf_index(m, g, a.K)] = (uint8_t)(se + 127);
       } else {
-        constexpr float kQ = DT == kInt8 ? 127.0f : 448.0f;
-        const float top = amax * rstd;
-        float sc;
-        // a NaN fails, which may be in either
-        if (amax >= 0x1p-100f && top >= 0x1p-100f && amax <= 0x1p100f && top <= 0x1p100f) {
-          sc = quotient(top, kQ, 1.0f / kQ);
-          const float f = quotient(kQ, amax, rcp(amax));
+        float sc, f;
+        if (group_factor<DT>(amax, rstd, sc, f)) {
           q.x = DT == kInt8 ? int8x4(t, f) : e4m3x4(t, f);
           q.y = DT == kInt8 ? int8x4(t + 4, f) : e4m3x4(t + 4, f);
-        } else {                               // the factor may not be a number
-          sc = group_scale<DT>(top);
+        } else {
           float y[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) y[e] = t[e] * rstd;

@@ -488,11 +488,18 @@ bq_status bq_moe_combine(const void* y, int64_t ldy, const int32_t* inv_perm,
  *   y[m, k] = r[m, k] / sqrt(mean_k r[m, k]^2 + eps) * (weight[k] + weight_offset)
  *   q, s    = the 1 x group_k quantisation of y, as bq_quant_act
  * y is fp32 and is quantised unrounded (a separate norm and bq_quant_act
- * would round it to bf16 in between).  x: bf16 [M, K] (row stride ldx >= K);
- * residual: bf16 [M, K] (row stride ldr) or NULL; weight: bf16 [K];
- * weight_offset: 0, or 1 for weights stored as their difference from 1.
- * q: codes [M, K] (row stride ldq), s: fp32 [ceil(K/group_k)][M]; a group with a y
- * that is not a number has a NaN scale.
+ * would round it to bf16 in between).  s is amax / Q in one IEEE division; a row's
+ * 1 / sqrt is off by a few units in the last place, as the order of its sum has it,
+ * and may differ by that between strides and alignments.  The codes are rounded to
+ * nearest even from r * (weight + weight_offset) times Q / its largest magnitude in
+ * the group, which is y / s without the row's factor: they do not depend on strides
+ * or alignment, and may be either neighbour where y / s lies within fp32's error of
+ * the middle between two codes.  The sum of squares is fp32: |r| up to 2^50, and for
+ * eps = 0 each row's largest from 2^-50 on.
+ * x: bf16 [M, K] (row stride ldx >= K); residual: bf16 [M, K] (row stride ldr) or
+ * NULL; weight: bf16 [K]; weight_offset: 0, or 1 for weights stored as their
+ * difference from 1.  q: codes [M, K] (row stride ldq), s: fp32
+ * [ceil(K/group_k)][M]; a group with a y that is not a number has a NaN scale.
  * res_out: r as bf16 [M, K] (row stride ldro), or NULL; it may be residual or
  * x itself (same pointer and stride).  h_out: y rounded to bf16 [M, K] (row
  * stride ldh), or NULL.  Other overlaps of inputs and outputs are not allowed.

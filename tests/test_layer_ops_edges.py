@@ -327,3 +327,23 @@ def test_mx_norm_with_values_that_are_not_numbers(L):                        # n
         assert not (q[[0, 2, 3, 4]][:, rest] & 0x7F == 0x7F).any()
         got.append((q, torch.from_numpy(e)))
     assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [bq.INT8, bq.FP8_E4M3])
+@pytest.mark.parametrize("w_off", [0.0, 1.0])
+@pytest.mark.parametrize("M,K,group", [(40, 4096, 128), (9, 512, 512), (7, 200, 8), (3, 20480, 256)])
+def test_norm_codes_do_not_depend_on_alignment(L, M, K, group, w_off, dtype):    # noqa: F811
+    """The same rows for the vector kernel and the other one: codes bit for bit, ties
+    included; scales up to the order of a row's sum (K terms) and its root."""
+    g = gen(K + group)
+    x = (randn(g, M, K) * 8).round().bfloat16()          # few distinct values: many exact halves
+    w = (1 + 0.25 * randn(g, K).round()).bfloat16() - w_off
+    x[M // 2] = 0
+    x[0, :group] *= 2.0 ** -40
+    q, s, h = bq.rmsnorm_quant(x, w, 1e-5, None, group, dtype, w_off, want_h=True)
+    q2, s2, h2 = bq.rmsnorm_quant(shifted(x), w, 1e-5, None, group, dtype, w_off, want_h=True)
+    assert torch.equal(q, q2)
+    rel = 2 * ref.norm_rel(K)
+    assert ((s.double() - s2.double()).abs() <= rel * s.double()).all()
+    assert ((h.double() - h2.double()).abs() <= (2 * ref.UBF16 + rel) * h.double().abs()).all()
