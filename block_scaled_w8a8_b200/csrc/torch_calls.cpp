@@ -125,6 +125,14 @@ double real(PyObject* o, const char* name) {
   return v;
 }
 
+// The truth of an argument; what Python raises on asking for it (a tensor of several
+// elements) goes on to the caller.
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw python_error();
+  return v == 1;
+}
+
 bool none(PyObject* o) { return o == Py_None; }
 
 // The tensors' device as the current one while the library launches.
@@ -179,7 +187,7 @@ PyObject* rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (x.dim() != 2) throw Bad{"x must be bfloat16 [M, K]"};
     const int64_t M = x.size(0), K = x.size(1), group = whole(a[4], "group_k");
     const int dtype = small(a[5], "dtype");
-    const bool mx = PyObject_IsTrue(a[12]) == 1;
+    const bool mx = truth(a[12]);
     if (group < 1) throw Bad{"group_k must be >= 1"};
     const int64_t ldx = rows(x, "x", at::kBFloat16, M, K, dev);
     void* w = dense(tensor(a[1], "weight"), "weight", at::kBFloat16, {K}, dev);
@@ -223,7 +231,7 @@ PyObject* rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!none(a[11])) {
       h = tensor(a[11], "h");
       ldh = rows(h, "h", at::kBFloat16, M, K, dev);
-    } else if (PyObject_IsTrue(a[7]) == 1) {
+    } else if (truth(a[7])) {
       h = fresh({M, K}, at::kBFloat16, x);
     }
     const float eps = (float)real(a[2], "eps"), off = (float)real(a[6], "weight_offset");
@@ -350,6 +358,7 @@ PyObject* kv_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
                   window = whole(a[13], "window");
     const float scale = none(a[11]) ? (float)(1.0 / std::sqrt((double)c.D))
                                     : (float)real(a[11], "scale");
+    const bool causal = truth(a[12]);
     size_t bytes = 0;
     bq_status st = bq_kv_attention_workspace_size(b.B, T, Hq, c.H, c.D, max_q, max_kv, c.page,
                                                   c.bt, &bytes);
@@ -366,7 +375,7 @@ PyObject* kv_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const On on(dev);
     st = bq_kv_attention(hq.p, hq.token, hq.head, b.off, b.lens, b.table, b.ld, b.cols, b.B, T, Hq,
                          c.H, c.D, max_q, max_kv, c.k, c.v, c.ks, c.vs, c.n_pages, c.page, c.bt,
-                         small(a[5], "dtype"), scale, PyObject_IsTrue(a[12]) == 1, window, ho.p,
+                         small(a[5], "dtype"), scale, causal, window, ho.p,
                          ho.token, ho.head, lse, ws.defined() ? ws.data_ptr() : nullptr, bytes,
                          on.stream);
     return st == BQ_OK ? THPVariable_Wrap(out) : status(st);

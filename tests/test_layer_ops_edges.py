@@ -347,3 +347,23 @@ def test_norm_codes_do_not_depend_on_alignment(L, M, K, group, w_off, dtype):   
     rel = 2 * ref.norm_rel(K)
     assert ((s.double() - s2.double()).abs() <= rel * s.double()).all()
     assert ((h.double() - h2.double()).abs() <= (2 * ref.UBF16 + rel) * h.double().abs()).all()
+
+
+# ---- host calls ----------------------------------------------------------------------
+
+@gpu
+def test_arguments_without_a_truth_value_are_refused(L):                     # noqa: F811
+    both = torch.tensor([True, False])
+    x, w = torch.ones(2, 128, dtype=torch.bfloat16, device="cuda"), torch.ones(128, dtype=torch.bfloat16,
+                                                                               device="cuda")
+    with pytest.raises(RuntimeError):
+        bq.rmsnorm_quant(x, w, want_h=both)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    c = bq.kv_cache(1, 1, 16, 64)
+    out = torch.full((1, 1, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    q = torch.ones_like(out)
+    args = (q, c, torch.tensor([0, 1], **i32), torch.ones(1, **i32), torch.zeros(1, 1, **i32), 1, 16)
+    with pytest.raises(RuntimeError):
+        bq.kv_attention(*args, causal=both, out=out)
+    assert (out == 7).all()
+    assert (bq.kv_attention(*args, causal=both[:1], out=out) == 0).all()
