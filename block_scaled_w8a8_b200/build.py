@@ -17,6 +17,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -24,6 +25,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libbq.so")
 EXT = os.path.join(PKG, "_torch_calls.so")
+EXT_STAMP = os.path.join(BUILD, "_torch_calls.stamp")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 # No fast-math, no flush-to-zero: quantisation must round like IEEE fp32.
@@ -92,22 +94,54 @@ def _link_ext(obj: str):
     os.replace(tmp, EXT)
 
 
+def _ext_stamp() -> str:
+    """What the extension fits besides its sources: the interpreter and torch."""
+    import torch
+    return f"python {sysconfig.get_config_var('SOABI')}, torch {torch.__version__}\n"
+
+
+def _fresh(path: str) -> bool:
+    return os.path.exists(path) and os.path.getmtime(path) >= _deps_mtime()
+
+
+def _ext_fresh() -> bool:
+    if not _fresh(EXT) or not os.path.exists(EXT_STAMP):
+        return False
+    with open(EXT_STAMP) as f:
+        return f.read() == _ext_stamp()
+
+
+def _build_ext():
+    try:
+        _link_ext(_compile_ext())
+        with open(EXT_STAMP, "w") as f:
+            f.write(_ext_stamp())
+    except (ImportError, OSError, RuntimeError) as e:
+        # the C ABI and the calls through ctypes do not need it; those that do raise
+        warnings.warn(f"{os.path.basename(EXT)} is not built (norm, rotary positions, cache and "
+                      f"attention cannot be called on torch tensors): {e}", RuntimeWarning,
+                      stacklevel=3)
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _deps_mtime()
-                         for f in (LIB, EXT)):
+    """Build what is out of date; raises if libbq.so cannot be built, warns if the
+    extension module (host compiler, torch's headers) cannot."""
+    lib, ext = force or not _fresh(LIB), force or not _ext_fresh()
+    if not lib and not ext:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
-    srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
-        ext = ex.submit(_compile_ext)
-        objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), srcs))
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
-    _link_ext(ext.result())
+    if lib:
+        srcs = sources()
+        with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+            objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), srcs))
+        tmp = LIB + f".tmp{os.getpid()}"
+        cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, LIB)
+    if ext:
+        _build_ext()
     return LIB
 
 
