@@ -1,6 +1,7 @@
 """The operators between two linears at the edges of their ranges: a long tail under
 a dominating key, scales far apart, zeros with a sign, values that are not numbers,
 more rows than a launch has CTAs."""
+import ctypes
 import math
 
 import pytest
@@ -367,3 +368,60 @@ def test_arguments_without_a_truth_value_are_refused(L):                     # n
         bq.kv_attention(*args, causal=both, out=out)
     assert (out == 7).all()
     assert (bq.kv_attention(*args, causal=both[:1], out=out) == 0).all()
+
+
+# ---- more rows than a launch has CTAs, workspaces ---------------------------------------
+
+@gpu
+@pytest.mark.parametrize("M,K,group,dtype,off", [
+    (1000, 20480, 256, bq.INT8, 0), (1000, 4096, 4096, bq.INT8, 0), (1000, 4096, 4096, bq.FP8_E4M3, 0),
+    (2500, 200, 100, bq.INT8, 0), (2500, 200, 100, bq.FP8_E4M3, 0), (2500, 256, 128, bq.INT8, 1),
+    (700, 14336, 128, bq.FP8_E4M3, 0)])
+def test_norm_of_more_rows_than_ctas(L, M, K, group, dtype, off):            # noqa: F811
+    """Every kernel goes through its loop over rows several times, in place of the residual."""
+    g = gen(M + K + group)
+    x, w = randn(g, M, K).bfloat16(), (1 + 0.2 * randn(g, K)).bfloat16()
+    x *= torch.exp2(torch.arange(M, device="cuda") % 7 - 3)[:, None]         # rows of different size
+    res = randn(g, M, K + 8).bfloat16()[:, off:off + K]
+    r, y = ref.rmsnorm(x, w, 1e-5, res)
+    q, s, ro = bq.rmsnorm_quant(x, w, 1e-5, res, group, dtype, res_out=res)
+    assert ro is res and torch.equal(res, r)
+    ref.check_codes(q, s, y, group, dtype, ref.norm_rel(K))
+
+
+@gpu
+def test_mx_norm_of_more_rows_than_ctas(L):                                  # noqa: F811
+    import gpu_util
+    M, K, g = 2000, 4096, gen(43)
+    x, w = randn(g, M, K).bfloat16(), (1 + 0.2 * randn(g, K)).bfloat16()
+    x *= torch.exp2(torch.arange(M, device="cuda") % 7 - 3)[:, None]
+    res = randn(g, M, K).bfloat16()
+    r, y = ref.rmsnorm(x, w, 1e-6, res)
+    q, sf, ro = bq.mx_rmsnorm_quant(x, w, 1e-6, res, res_out=res)
+    assert ro is res and torch.equal(res, r)
+    rel = ref.norm_rel(K)
+    e = torch.from_numpy(gpu_util.mx_sf_rows(sf, M, K)).cuda().double()
+    a = y.view(M, K // 32, 32)
+    low, high = (torch.floor(torch.log2(a.abs().amax(2) * f)) + 119 for f in (1 - 2 * rel, 1 + 2 * rel))
+    assert ((e >= low) & (e <= high)).all()
+    n = (a / torch.exp2(e - 127)[..., None]).clamp(-448, 448)
+    tol = torch.maximum(n.abs() * 2.0 ** -4, torch.full_like(n, 2.0 ** -10)) + n.abs() * 2 * rel
+    assert ((ref.decode(q, 1).view(a.shape) - n).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("B,T,Hq,Hkv,D,max_q,max_kv", [
+    (1, 1, 32, 8, 128, 1, 1 << 17), (2, 2, 4, 4, 64, 1, 1 << 17), (1, 64, 4, 4, 128, 64, 6000),
+    (1, 1, 8, 8, 96, 1, 4000)])
+def test_split_keys_have_a_workspace(L, B, T, Hq, Hkv, D, max_q, max_kv):    # noqa: F811
+    """Long keys of few rows are split, so the workspace holds at least two parts of each
+    row behind the 64 KiB left alone; it grows with the keys and refuses less."""
+    n = bq.kv_attention_workspace_size(B, T, Hq, Hkv, D, max_q, max_kv, 64, 16)
+    assert n >= 65536 + 2 * T * Hq * (D + 2) * 4
+    assert bq.kv_attention_workspace_size(B, T, Hq, Hkv, D, max_q, 16, 64, 16) <= n
+    fake = ctypes.c_void_p
+    cols = -(-max_kv // 64)
+    args = [fake(0x1000), Hq * D, D, fake(0x1000), fake(0x1000), fake(0x1000), cols, cols, B, T, Hq, Hkv, D,
+            max_q, max_kv, *[fake(0x1000)] * 4, 16, 64, 16, 0, 0.1, 1, 0, fake(0x9000), Hq * D, D, None]
+    for ws, size, status in [(None, 0, bq.ERR_WORKSPACE), (fake(0x10000), n - 1, bq.ERR_WORKSPACE),
+                             (fake(0x10004), n, bq.ERR_ALIGNMENT)]:
+        assert L.bq_kv_attention(*args, ws, size, None) == status
