@@ -959,8 +959,9 @@ bq_status bq_kv_attention(const void* q, int64_t ldq, int64_t hq, const int32_t*
   if (T == 0 || B == 0) return ok();
   BQ_CHECK_ARG(q && seq_offsets && kv_lens && out, "q, seq_offsets, kv_lens and out must not be "
                                                    "NULL");
-  BQ_CHECK_ARG(table_cols == 0 || n_pages == 0 ||
-                   (page_table && k_codes && v_codes && k_scales && v_scales),
+  // lengths are only known on the device: the table is read even if there are no pages
+  BQ_CHECK_ARG(table_cols == 0 ||
+                   (page_table && (n_pages == 0 || (k_codes && v_codes && k_scales && v_scales))),
                "page_table and the cache arrays must not be NULL");
   const size_t parts = bq::attn_workspace_bytes(B, T, Hq, Hkv, D, max_q_len, max_kv_len,
                                                 page_size, block_t);

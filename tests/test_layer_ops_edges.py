@@ -425,3 +425,12 @@ def test_split_keys_have_a_workspace(L, B, T, Hq, Hkv, D, max_q, max_kv):    # n
     for ws, size, status in [(None, 0, bq.ERR_WORKSPACE), (fake(0x10000), n - 1, bq.ERR_WORKSPACE),
                              (fake(0x10004), n, bq.ERR_ALIGNMENT)]:
         assert L.bq_kv_attention(*args, ws, size, None) == status
+
+
+def test_attention_refuses_a_page_table_that_is_not_there(L):                # noqa: F811
+    """Also for a cache without pages: lengths are on the device, so the table is read."""
+    p = ctypes.c_void_p
+    for n_pages, arrays in ((0, None), (16, p(0x1000))):
+        args = [p(0x1000), 512, 128, p(0x1000), p(0x1000), None, 8, 8, 2, 4, 4, 2, 128, 2, 512, *[arrays] * 4,
+                n_pages, 64, 16, 0, 0.1, 1, 0, p(0x9000), 512, 128, None, p(0x10000), 1 << 40, None]
+        assert L.bq_kv_attention(*args) == bq.ERR_INVALID_ARG
