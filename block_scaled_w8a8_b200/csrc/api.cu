@@ -913,7 +913,9 @@ bq_status bq_kv_append(const void* k, int64_t ldk, int64_t hk, const void* v, in
   return ok();
 }
 
-static bq_status attn_check(int64_t Hq, int64_t Hkv, int64_t D, int64_t max_q_len,
+// max_q_len is brought below kAttnMaxRows rows of a key head: the kernels number them in
+// 32 bits, and no sequence has more than the call's T rows.
+static bq_status attn_check(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t& max_q_len,
                             int64_t max_kv_len) {
   BQ_CHECK_ARG(Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0,
                "Hq (%lld) must be a multiple of Hkv (%lld)", (long long)Hq, (long long)Hkv);
@@ -921,6 +923,11 @@ static bq_status attn_check(int64_t Hq, int64_t Hkv, int64_t D, int64_t max_q_le
   if (D < 1 || D > 256 || Hq > 65535 || max_q_len > INT32_MAX || max_kv_len > INT32_MAX)
     return fail(BQ_ERR_UNSUPPORTED,
                 "attention takes D in [1, 256], Hq <= 65535 and lengths within int32");
+  const int64_t most = bq::kAttnMaxRows / (Hq / Hkv);
+  if (std::min(T, max_q_len) > most)
+    return fail(BQ_ERR_UNSUPPORTED, "attention takes up to %lld rows of a sequence and key head",
+                (long long)bq::kAttnMaxRows);
+  max_q_len = std::min(max_q_len, most);
   return BQ_OK;
 }
 
@@ -930,10 +937,12 @@ bq_status bq_kv_attention_workspace_size(int64_t B, int64_t T, int64_t Hq, int64
                                          int64_t block_t, size_t* bytes) {
   BQ_CHECK_ARG(bytes, "bytes must not be NULL");
   bq_status st = kv_check(0, 0, B, T, Hkv, D, 0, page_size, block_t, BQ_INT8);
-  if (st == BQ_OK) st = attn_check(Hq, Hkv, D, max_q_len, max_kv_len);
+  if (st == BQ_OK) st = attn_check(T, Hq, Hkv, D, max_q_len, max_kv_len);
   if (st != BQ_OK) return st;
   const size_t n = bq::attn_workspace_bytes(B, T, Hq, Hkv, D, max_q_len, max_kv_len, page_size,
                                             block_t);
+  if (n > bq::kAttnMaxWorkspace)
+    return fail(BQ_ERR_UNSUPPORTED, "the split keys' workspace would pass 2^60 bytes");
   *bytes = n ? n + bq::kDecodeCounterBytes : 0;
   return ok();
 }
@@ -948,7 +957,7 @@ bq_status bq_kv_attention(const void* q, int64_t ldq, int64_t hq, const int32_t*
                           int64_t ho, float* lse, void* workspace, size_t workspace_bytes,
                           void* stream) {
   bq_status st = kv_check(ld_table, table_cols, B, T, Hkv, D, n_pages, page_size, block_t, dtype);
-  if (st == BQ_OK) st = attn_check(Hq, Hkv, D, max_q_len, max_kv_len);
+  if (st == BQ_OK) st = attn_check(T, Hq, Hkv, D, max_q_len, max_kv_len);
   if (st != BQ_OK) return st;
   BQ_CHECK_ARG(std::isfinite(scale), "scale must be finite");
   BQ_CHECK_ARG(window >= 0 && (window == 0 || causal), "a window needs causal attention");
@@ -965,6 +974,8 @@ bq_status bq_kv_attention(const void* q, int64_t ldq, int64_t hq, const int32_t*
                "page_table and the cache arrays must not be NULL");
   const size_t parts = bq::attn_workspace_bytes(B, T, Hq, Hkv, D, max_q_len, max_kv_len,
                                                 page_size, block_t);
+  if (parts > bq::kAttnMaxWorkspace)
+    return fail(BQ_ERR_UNSUPPORTED, "the split keys' workspace would pass 2^60 bytes");
   const size_t need = parts ? parts + bq::kDecodeCounterBytes : 0;
   if (need > 0 && (workspace == nullptr || workspace_bytes < need))
     return fail(BQ_ERR_WORKSPACE, "bq_kv_attention needs %zu workspace bytes, got %zu", need,

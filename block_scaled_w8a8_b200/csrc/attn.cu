@@ -309,8 +309,7 @@ cudaError_t launch_pdl(void (*kernel)(Args...), dim3 grid, int threads, cudaStre
 cudaError_t launch_any(const AttnArgs& a, const AttnParts& p, cudaStream_t st) {
   const int64_t rows = (int64_t)a.max_q * (a.Hq / a.c.H);
   const int64_t tiles = std::max<int64_t>(1, (rows + kAnyRows - 1) / kAnyRows);
-  const dim3 grid((unsigned)std::min<int64_t>(tiles * a.b.B * p.splits, (int64_t)INT32_MAX + 1),
-                  (unsigned)a.c.H);
+  const dim3 grid((unsigned)attn_grid({tiles, a.b.B, p.splits}), (unsigned)a.c.H);
   return a.c.dtype == kInt8
              ? launch_pdl(attn_any_kernel<kInt8>, grid, kAnyWarps * 32, st, a, p, (int)tiles)
              : launch_pdl(attn_any_kernel<kFp8>, grid, kAnyWarps * 32, st, a, p, (int)tiles);

@@ -2,6 +2,8 @@
 // the keys over CTAs and its workspace, and the kernels' launchers.
 #pragma once
 
+#include <initializer_list>
+
 #include "layer_ops.h"
 
 namespace bq {
@@ -19,7 +21,20 @@ struct AttnParts {
 };
 
 inline size_t attn_part_bytes(int64_t rows, int splits, int64_t D) {
-  return splits <= 1 ? 0 : (size_t)rows * (size_t)splits * (size_t)(D + 2) * sizeof(float) + 16;
+  if (splits <= 1) return 0;
+  const size_t one = (size_t)splits * (size_t)(D + 2) * sizeof(float);
+  if ((size_t)rows > kAttnMaxWorkspace / one) return kAttnMaxWorkspace + 1;
+  return (size_t)rows * one + 16;
+}
+
+// A grid's CTAs from its factors; INT32_MAX + 1, which no launch takes, for more.
+inline int64_t attn_grid(std::initializer_list<int64_t> factors) {
+  int64_t n = 1;
+  for (int64_t f : factors) {
+    if (f > 0 && n > INT32_MAX / f) return (int64_t)INT32_MAX + 1;
+    n *= f;
+  }
+  return n;
 }
 
 cudaError_t launch_attn_merge(const AttnArgs& a, const AttnParts& p, cudaStream_t st);

@@ -439,8 +439,8 @@ template <int DT, int D, int UNI>
 cudaError_t launch_t(const AttnArgs& a, const AttnParts& p, cudaStream_t st) {
   const int64_t rows = (int64_t)a.max_q * (a.Hq / a.c.H);
   const int64_t tiles = (rows + R - 1) / R;
-  const int64_t x = tiles * a.b.B * p.splits;
-  if (x > INT32_MAX || tiles > INT32_MAX) return cudaErrorInvalidConfiguration;
+  const int64_t x = attn_grid({tiles, a.b.B, p.splits});
+  if (x > INT32_MAX) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)x, (unsigned)a.c.H);
   cfg.blockDim = dim3(kWarps * 32);

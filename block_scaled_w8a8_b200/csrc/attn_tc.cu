@@ -762,7 +762,7 @@ cudaError_t launch_t(const AttnArgs& a, const AttnParts& p, cudaStream_t st) {
     ready[dev] = true;
   }
   const int64_t tiles = attn_tc_tiles(a.max_q, a.Hq / a.c.H);
-  const int64_t grid = tiles * a.b.B * p.splits * a.c.H;
+  const int64_t grid = attn_grid({tiles, a.b.B, p.splits, a.c.H});
   if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);

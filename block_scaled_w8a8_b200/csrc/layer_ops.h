@@ -86,6 +86,11 @@ struct AttnArgs {
   unsigned* status;
 };
 
+// Rows (tokens x heads of its group) of a sequence and key head that the kernels number.
+constexpr int64_t kAttnMaxRows = 1 << 30;
+constexpr size_t kAttnMaxWorkspace = (size_t)1 << 60;
+
+// Above kAttnMaxWorkspace if it would be larger than that.
 size_t attn_workspace_bytes(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
                             int64_t max_q, int64_t max_kv, int64_t page, int64_t bt);
 cudaError_t launch_kv_attention(const AttnArgs& a, void* ws, cudaStream_t st);

@@ -620,7 +620,8 @@ bq_status bq_kv_attention_workspace_size(int64_t B, int64_t T, int64_t Hq, int64
  * ho (no overlap with q); lse: fp32 [T][Hq] or NULL.  max_q_len and max_kv_len
  * bound every sequence's rows and length (a longer sequence is skipped and
  * recorded); they choose the kernel and the workspace, so a captured call
- * stays valid while lengths grow up to them.  D <= 256.
+ * stays valid while lengths grow up to them.  D <= 256, and at most 2^30 rows (tokens
+ * times Hq / Hkv) of a sequence and key head.
  * workspace: at least bq_kv_attention_workspace_size bytes, 16-byte aligned, no
  * initialisation, nothing kept in it; calls sharing one must not overlap on
  * the GPU.  Its first 64 KiB are left untouched, so the buffer of bq_gemm can

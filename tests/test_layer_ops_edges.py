@@ -434,3 +434,32 @@ def test_attention_refuses_a_page_table_that_is_not_there(L):                # n
         args = [p(0x1000), 512, 128, p(0x1000), p(0x1000), None, 8, 8, 2, 4, 4, 2, 128, 2, 512, *[arrays] * 4,
                 n_pages, 64, 16, 0, 0.1, 1, 0, p(0x9000), 512, 128, None, p(0x10000), 1 << 40, None]
         assert L.bq_kv_attention(*args) == bq.ERR_INVALID_ARG
+
+
+def test_attention_refuses_sizes_that_its_kernels_cannot_number(L):          # noqa: F811
+    """Rows of a key head are numbered in 32 bits, and a workspace's size must not wrap round."""
+    n = ctypes.c_size_t(0)
+
+    def size(B, T, Hq, Hkv, D, max_q, max_kv):
+        return L.bq_kv_attention_workspace_size(B, T, Hq, Hkv, D, max_q, max_kv, 64, 16, ctypes.byref(n))
+    assert size(1, 1 << 28, 8, 1, 64, 1 << 28, 128) == bq.ERR_UNSUPPORTED
+    assert size(1, 1 << 28, 8, 1, 64, 1 << 27, 128) == bq.OK
+    assert size(1, 4, 8, 1, 64, (1 << 31) - 1, 128) == bq.OK         # a bound far above the call's rows
+    assert size(1, (1 << 31) - 2, 65535, 65535 // 3, 255, 1, (1 << 31) - 1) == bq.ERR_UNSUPPORTED
+    p = ctypes.c_void_p
+    args = [p(0x1000), 512, 64, p(0x1000), p(0x1000), p(0x1000), 8, 8, 1, 1 << 28, 8, 1, 64, 1 << 28, 512,
+            *[p(0x1000)] * 4, 16, 64, 16, 0, 0.1, 1, 0, p(0x9000), 512, 64, None, p(0x10000), 1 << 62, None]
+    assert L.bq_kv_attention(*args) == bq.ERR_UNSUPPORTED
+
+
+@gpu
+@pytest.mark.parametrize("D", [128, 64, 40])
+def test_attention_with_a_row_bound_far_above_the_rows(L, D):                # noqa: F811
+    g = gen(D)
+    off, ln, table, count = make_batch(g, [3], [300], 32)
+    c = random_cache(g, count, 1, 32, D, 16, bq.INT8)
+    q = randn(g, 3, 8, D).bfloat16()
+    want, _, tol, _ = ref.attention(q, c.k, c.v, c.ks, c.vs, off, ln, table, bq.INT8)
+    got = bq.kv_attention(q, c, off, ln, table, 2 ** 31 - 1, 300)
+    bq.check_device_status()
+    assert ((got.double() - want).abs() <= tol).all()
