@@ -320,8 +320,8 @@ enum class Path { kAny, kDecode, kTc };
 
 // Rows per key head up to which the streaming kernel is taken; it reads the codes
 // once for 8 rows, the tensor core kernel once for 256 but with a dearer start.  16
-// sequences of 8192 keys: 16 rows 121 and 163 us, 24 rows 156 and 163; 1 of 65536:
-// 16 rows 75 and 88, 24 rows 94 and 88; 1 of 4096: 24 rows 17 and 22 us.
+// sequences of 8192 keys: 16 rows 125 and 165 us, 24 rows 163 and 165, 32 rows 217 and
+// 165; 1 of 65536: 16 rows 69 and 88, 24 rows 97 and 88; 1 of 4096: 24 rows 17 and 22 us.
 constexpr int64_t kDecodeRows = 24;
 
 Path plan_path(int64_t D, int64_t page, int64_t rows) {

@@ -14,9 +14,9 @@
 //                 one row of D bytes); a byte permute pairs two tokens' codes.
 //                 P^T is S^T's accumulator, transposed in registers (movmatrix).
 // More rows are more row tiles, side by side in the grid, whose codes come from L2:
-// 16 x 8192 keys, 8 rows 78 us, 16 rows 120 us (two row tiles in one CTA, whose
-// registers leave room for half as many warps: 134 us).
-// 64 x up to 8192 keys, 32 heads over 8 of dim 128: 139 to 144 us, 4.8 TB/s.
+// 16 x 8192 keys, 8 rows 73 us, 16 rows 124 us (two row tiles in one CTA, whose
+// registers leave room for half as many warps: slower by a tenth).
+// 64 x up to 8192 keys, 32 heads over 8 of dim 128: 142 us, 4.7 TB/s.
 // A group's registers take the next group's codes as soon as the product that
 // reads them has been issued, so a warp has about 4 KB under way and needs no
 // second set of registers.
@@ -68,9 +68,10 @@ struct Place {
 };
 
 // UNI: what of the tokens shares its scales and its page: 16 a group (block_t a
-// multiple of 16), 32 a step of two groups (D = 64, block_t a multiple of 32), 0
-// nothing.  2 x up to 131071 keys of dim 64, block_t 32: 68, 64, 56 us with 0, 16,
-// 32; 64 x up to 8192 keys of dim 128, block_t 64: 143, 138 us with 0, 16.
+// multiple of 16), 32 a step of two groups (block_t a multiple of 32), 0 nothing.  2 x
+// up to 131071 keys of dim 64, block_t 32: 69, 65, 57 us with 0, 16, 32.  Dim 128, with
+// one group a step, has no use for it (64 x up to 8192 keys, block_t 64: 141.4, 142.6 us
+// with 0, 16; 16 x 8192, block_t 16: 73, 75 us).
 template <int DT, int D, int UNI>
 __global__ void __launch_bounds__(kWarps * 32, 4)
 attn_decode_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles) {
@@ -455,9 +456,11 @@ cudaError_t launch_t(const AttnArgs& a, const AttnParts& p, cudaStream_t st) {
 
 template <int DT, int D>
 cudaError_t launch_d(const AttnArgs& a, const AttnParts& p, cudaStream_t st) {
-  if constexpr (D == 64)
+  if constexpr (D == 64) {
     if (a.c.bt % 32 == 0) return launch_t<DT, D, 32>(a, p, st);
-  return a.c.bt % 16 == 0 ? launch_t<DT, D, 16>(a, p, st) : launch_t<DT, D, 0>(a, p, st);
+    if (a.c.bt % 16 == 0) return launch_t<DT, D, 16>(a, p, st);
+  }
+  return launch_t<DT, D, 0>(a, p, st);
 }
 
 template <int DT>
