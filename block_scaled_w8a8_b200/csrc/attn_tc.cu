@@ -33,10 +33,11 @@
 // attn_decode.cu.  Keys that no row of the CTA sees have zero codes and lg2 vs =
 // -inf, so no stale byte enters a sum.
 //
-// Measured: a prompt of 8192 tokens (32 heads over 8, dim 128) 645 us, 853 TFLOP/s
-// of the two products over the pairs that causality leaves.  Bound by the tensor
-// cores as they are fed: with neither softmax nor conversion in the way the
-// products alone take 508 us, since a score product of 64 keys reads as much of Q
+// Measured: a prompt of 8192 tokens (32 heads over 8, dim 128) 633 us, 869 TFLOP/s
+// of the two products over the pairs that causality leaves, for some milliseconds of
+// calls one behind the other; 677 us, 812 TFLOP/s, in a run of hundreds, in which the
+// card's power limit lowers its clock.  Bound by the tensor cores as they are fed: with
+// neither softmax nor conversion in the way the products alone take 508 us, since a score product of 64 keys reads as much of Q
 // from shared memory as one of 128 would.  128 scores at a time halve that, but
 // tensor memory then holds one block a row tile, so that the products wait for the
 // softmax and the other way round (723 us).  The softmax adds 85 us, the conversion
@@ -214,8 +215,8 @@ __device__ __forceinline__ void fence_async_shared() {
 // UNI: aligned tokens that share their scales: 64 (a score block), 16 or 0, as
 // block_t is a multiple of them.  With 16 the scales of a tile are eight entries
 // {cs, lg2 vs, 1 / vs, -}, with 64 a score block has one of them.  Prompt of 8192,
-// block_t 64: 912, 688, 645 us with 0, 16, 64; three chunks of 513 over 6000 keys,
-// block_t 16: 226, 173 us with 0, 16.
+// block_t 64: 902, 688, 631 us with 0, 16, 64; three chunks of 513 over 6000 keys,
+// block_t 16: 215, 174 us with 0, 16.
 template <int DT, int D, int UNI>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_tc_kernel(const AttnArgs a, const AttnParts parts, const int row_tiles) {

@@ -202,8 +202,8 @@ __global__ void __launch_bounds__(kAnyThreads) norm_any_kernel(const NormArgs a)
 // the whole row): a CTA per row, V vectors of 8 elements a thread, everything in
 // registers, one barrier a row.  Memory-bound: x and the residual are read once,
 // the sum, the codes and the scales written once; the next row is under way while
-// one is reduced (up to 16384 columns).  With a residual, 4096 x 4096 to INT8: 23.7 us,
-// 5.0 TB/s; 2047 x 14336 to MXFP8: 36.1 us, 5.7 TB/s: what it issues (three quarters
+// one is reduced (up to 16384 columns).  With a residual, 4096 x 4096 to INT8: 23.2 us,
+// 5.1 TB/s; 2047 x 14336 to MXFP8: 35.8 us, 5.7 TB/s: what it issues (three quarters
 // of the issue slots) stands in the way of the rest.  In place is safe: a row is loaded
 // and stored by one CTA, each element by one thread, loads first.
 // INT8: fma(t, Q / max |t|, 1.5 * 2^23) rounds to nearest even and leaves the code in
@@ -389,14 +389,14 @@ cudaError_t launch_any(const NormArgs& a, cudaStream_t st) {
 
 template <int DT>
 cudaError_t launch_dt(const NormArgs& a, cudaStream_t st) {
-  // odd widths, strides and groups (4096 x 4096: 89 us, the vector kernel 24 us)
+  // odd widths, strides and groups (4096 x 4096: 88 us, the vector kernel 23 us)
   if (!vec_ok(a)) return launch_any<DT>(a, st);
   // Few rows: a vector a thread, for latency; many: more loads in flight a thread
   // (1, 2 vectors: 16 x 2048 2.2, 2.6 us, 148 x 4096 2.7, 2.9 us, 148 x 8192 3.6, 3.4 us,
   // 4096 x 2048 14.0, 13.7 us, 4096 x 8192 46, 43 us).  A CTA of 1024 threads ends at
   // 16384 elements; the wider rows' eight vectors cost up to half more where both
-  // could be taken (4096 x 14336: 111, 74 us), a sixth of the other kernel's time (2048 x
-  // 32768: 116, 682 us).
+  // could be taken (4096 x 14336: 111, 74 us), a fifth of the other kernel's time (2048 x
+  // 32768: 118, 563 us).
   if (a.M <= 148 && a.K <= 4096) return launch_vec<DT, 1>(a, st);
   return a.K <= 16384 ? launch_vec<DT, 2>(a, st) : launch_vec<DT, 8>(a, st);
 }

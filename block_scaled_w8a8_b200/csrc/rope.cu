@@ -74,7 +74,8 @@ __global__ void __launch_bounds__(256) rope_any_kernel(const RopeArgs a) {
 // pair costs beyond fp32), then turn 16 bytes of each half (or four neighbouring
 // pairs) of all heads; the first of them are under way while the angles are formed.
 // Memory-bound: every byte is read and written once.  8191 tokens x 40 heads of 128:
-// 31.5 us, 5.3 TB/s (half of each head turned: 32.8 us); 8 heads of 64: 7.2 us.
+// neighbouring pairs 31.0 us, 5.4 TB/s, half layout 38.6 us, 4.3 TB/s; half of each head
+// turned 32.2 and 40.5 us; 8 heads of 64 6.6 us (half layout).
 constexpr int kVecThreads = 256;
 
 template <bool INTER>
@@ -180,7 +181,8 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st) {
   cfg.numAttrs = 1;
   if (vec_ok(a)) {
     // many tokens: as many a CTA as one round of its threads has angles for (one token a
-    // CTA: 8191 x 40 heads, half turned 38 us instead of 33, 8 heads of 64 27 instead of 19)
+    // CTA: 8191 x 40 heads, half layout 48.8 us instead of 38.6, neighbouring pairs, half
+    // turned 34.3 instead of 32.1, 8 heads of 64 26.1 instead of 6.6)
     const int64_t half = std::max<int64_t>(1, a.rot / 2);
     int64_t tt = std::max<int64_t>(1, kVecThreads / half);
     tt = std::min<int64_t>(tt, std::max<int64_t>(1, a.T / (148 * 8)));
@@ -193,7 +195,8 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st) {
                            : cudaLaunchKernelEx(&cfg, rope_vec_kernel<false>, a, (int)tt);
     }
   }
-  // odd widths and strides (8191 tokens x 40 heads: 183 us, the vector kernel 33 us)
+  // odd widths and strides (8191 tokens x 40 heads, 24 of 128 dimensions turned in half
+  // layout: 216 us, 64 of them in the vector kernel 40 us)
   const int64_t work = a.T * a.H * (a.D - a.rot / 2);
   cfg.gridDim = dim3((unsigned)std::min<int64_t>((work + 255) / 256, 148 * 16));
   cfg.blockDim = dim3(256);

@@ -538,6 +538,9 @@ typedef enum bq_rope_scaling {
  * rotations r_i = orig_max_pos * turns[i] and g = clamp((r_i - beta_slow) /
  * (beta_fast - beta_slow), 0, 1), theta_i becomes (1 - g) theta_i / factor +
  * g theta_i, and mscale = 1 + 0.1 ln(factor); mscale is 1 for the others.
+ * (Checkpoints whose configuration blends linearly in the pair's index, between
+ * the indices where r_i is beta_fast and beta_slow, need frequencies of the
+ * caller's own: bq_rope takes any.)
  * rot_dim even and >= 2 (>= 4 for BQ_ROPE_NTK), base > 1, factor >= 1,
  * and for BQ_ROPE_YARN orig_max_pos >= 1 and beta_fast > beta_slow. */
 bq_status bq_rope_frequencies(int64_t rot_dim, double base, int scaling, double factor,
