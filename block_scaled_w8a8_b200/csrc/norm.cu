@@ -102,14 +102,6 @@ __device__ __forceinline__ float largest(float amax, float v) {
   return DT == kMxFp8 ? fmaxf(amax, fabsf(v)) : max_nan(amax, fabsf(v));
 }
 
-// Four codes of y * inv, |y * inv| <= 127 (1 + 2^-22): round to nearest even.
-__device__ __forceinline__ uint32_t int8x4(const float* y, float inv) {
-  uint32_t b[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) b[e] = __float_as_uint(fmaf(y[e], inv, 12582912.0f));
-  return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
-}
-
 __device__ __forceinline__ uint32_t e4m3x4(const float* y, float inv) {
   unsigned short lo, hi;     // the first source operand lands in the upper byte
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(y[1] * inv), "f"(y[0] * inv));
@@ -117,20 +109,62 @@ __device__ __forceinline__ uint32_t e4m3x4(const float* y, float inv) {
   return (uint32_t)lo | (uint32_t)hi << 16;
 }
 
+// Q / max |t| in two parts.  t f is then correctly rounded, so that a quotient that lies
+// in the middle between two codes is exactly there and goes to the even one; with one
+// part all such values of a group went the way of its rounding.  (4096 x 4096 to
+// INT8: 23.2 us with one part, 23.7 with two.)
+struct Factor {
+  float hi, lo;
+};
+
+__device__ __forceinline__ float times(float t, const Factor& f) {
+  return fmaf(t, f.hi, __fmul_rn(t, f.lo));
+}
+
+__device__ __forceinline__ uint64_t times2(const float* t, const Factor& f) {
+  const uint64_t x = pair(__float_as_uint(t[0]), __float_as_uint(t[1]));
+  return sm100::fma2(x, pair(__float_as_uint(f.hi), __float_as_uint(f.hi)),
+                     mul2(x, pair(__float_as_uint(f.lo), __float_as_uint(f.lo))));
+}
+
+// Four codes of t f, |t f| <= Q: round to nearest even.  INT8: the sum with 1.5 * 2^23
+// leaves the code in the low byte, with no conversion unit involved.
+__device__ __forceinline__ uint32_t int8x4(const float* t, const Factor& f) {
+  constexpr uint32_t kMagic = 0x4B400000u;
+  const uint64_t a = sm100::add2(times2(t, f), pair(kMagic, kMagic));
+  const uint64_t b = sm100::add2(times2(t + 2, f), pair(kMagic, kMagic));
+  return __byte_perm(__byte_perm((uint32_t)a, (uint32_t)(a >> 32), 0x0040),
+                     __byte_perm((uint32_t)b, (uint32_t)(b >> 32), 0x0040), 0x5410);
+}
+
+__device__ __forceinline__ uint32_t e4m3x4(const float* t, const Factor& f) {
+  float q[4];
+#pragma unroll
+  for (int e = 0; e < 4; e += 2) {
+    const uint64_t x = times2(t + e, f);
+    q[e] = __uint_as_float((uint32_t)x);
+    q[e + 1] = __uint_as_float((uint32_t)(x >> 32));
+  }
+  return e4m3x4(q, 1.0f);
+}
+
 // Scale of an INT8 or FP8 group and the factor of its codes from amax = max |t|, where
 // y = t rstd and t = r (w + w_off): rstd falls out of y / s, so the codes are those of
-// t Q / max |t|, in which only Q / max |t| and the product round, and the scale is
-// max |t| rstd / Q.  Both kernels go by it, so that codes do not depend on the order
+// t Q / max |t|, and the scale is max |t| rstd / Q.  Both kernels go by it, so that codes do not depend on the order
 // of a row's sum, nor on strides and alignment.  False where the factor may not be a
 // number; the codes are then those of y / s, divided.
 template <int DT>
-__device__ __forceinline__ bool group_factor(float amax, float rstd, float& sc, float& f) {
+__device__ __forceinline__ bool group_factor(float amax, float rstd, float& sc, Factor& f) {
   constexpr float kQ = DT == kInt8 ? 127.0f : 448.0f;
   const float top = amax * rstd;
   // a NaN fails, which may be in either
   if (amax >= 0x1p-100f && top >= 0x1p-100f && amax <= 0x1p100f && top <= 0x1p100f) {
     sc = quotient(top, kQ, 1.0f / kQ);
-    f = quotient(kQ, amax, rcp(amax));
+    const float r = rcp(amax);
+    // kQ r is off by at most 3 units in the last place (r by one); from below, so that
+    // the rest is positive and a zero keeps its sign
+    f.hi = __uint_as_float(__float_as_uint(kQ * r) - 4);
+    f.lo = fmaf(-f.hi, amax, kQ) * r;
     return true;
   }
   sc = group_scale<DT>(top);
@@ -173,13 +207,14 @@ __global__ void __launch_bounds__(kAnyThreads) norm_any_kernel(const NormArgs a)
                                      (bf16_bits_to_float(a.w[k]) + a.w_off));
       amax = warp_max_nan(amax);                                   // of t, y = t rstd
       float sc = 0.f, inv = 0.f;
+      Factor f{};
       bool fast = false;
       if (DT == kMxFp8) {
         const int se = mx_exponent(fmaxf(amax * rstd, 0.f));       // 0 for a row that is all NaN
         inv = __uint_as_float((uint32_t)(127 - se) << 23);   // 2^-se, exact
         if (lane == 0) a.sf[mx_sf_index(m, g, a.K)] = (uint8_t)(se + 127);
       } else {
-        fast = group_factor<DT>(amax, rstd, sc, inv);
+        fast = group_factor<DT>(amax, rstd, sc, f);
         if (lane == 0) a.s[g * a.M + m] = sc;
       }
       for (int64_t k = k0 + lane; k < k1; k += 32) {
@@ -188,9 +223,9 @@ __global__ void __launch_bounds__(kAnyThreads) norm_any_kernel(const NormArgs a)
         if (DT == kMxFp8)
           a.q[m * a.ldq + k] = (uint8_t)(e4m3x2_code(y * inv, 0.f, 1.0f) & 0xFFu);
         else if (DT == kInt8 && fast)
-          a.q[m * a.ldq + k] = (uint8_t)__float_as_uint(fmaf(t, inv, 12582912.0f));
+          a.q[m * a.ldq + k] = (uint8_t)__float_as_uint(__fadd_rn(times(t, f), 12582912.0f));
         else
-          a.q[m * a.ldq + k] = fast ? one_code<DT>(t * inv, 1.0f) : one_code<DT>(y, sc);
+          a.q[m * a.ldq + k] = fast ? one_code<DT>(times(t, f), 1.0f) : one_code<DT>(y, sc);
         if (a.h) a.h[m * a.ldh + k] = float_to_bf16_bits(y);
       }
     }
@@ -202,12 +237,10 @@ __global__ void __launch_bounds__(kAnyThreads) norm_any_kernel(const NormArgs a)
 // the whole row): a CTA per row, V vectors of 8 elements a thread, everything in
 // registers, one barrier a row.  Memory-bound: x and the residual are read once,
 // the sum, the codes and the scales written once; the next row is under way while
-// one is reduced (up to 16384 columns).  With a residual, 4096 x 4096 to INT8: 23.2 us,
-// 5.1 TB/s; 2047 x 14336 to MXFP8: 35.8 us, 5.7 TB/s: what it issues (three quarters
+// one is reduced (up to 16384 columns).  With a residual, 4096 x 4096 to INT8: 23.7 us,
+// 5.0 TB/s; 2047 x 14336 to MXFP8: 35.8 us, 5.7 TB/s: what it issues (three quarters
 // of the issue slots) stands in the way of the rest.  In place is safe: a row is loaded
 // and stored by one CTA, each element by one thread, loads first.
-// INT8: fma(t, Q / max |t|, 1.5 * 2^23) rounds to nearest even and leaves the code in
-// the low byte, with no conversion unit involved.
 template <int DT, int V>
 __global__ void __launch_bounds__(V <= 2 ? 1024 : 512)
 norm_vec_kernel(const NormArgs a, const int lpg) {       // lpg: lanes of a group, 0 = the row
@@ -311,7 +344,8 @@ norm_vec_kernel(const NormArgs a, const int lpg) {       // lpg: lanes of a grou
         q.y = e4m3x4(y + 4, inv);
         if (first) a.sf[mx_sf_index(m, g, a.K)] = (uint8_t)(se + 127);
       } else {
-        float sc, f;
+        float sc;
+        Factor f;
         if (group_factor<DT>(amax, rstd, sc, f)) {
           q.x = DT == kInt8 ? int8x4(t, f) : e4m3x4(t, f);
           q.y = DT == kInt8 ? int8x4(t + 4, f) : e4m3x4(t + 4, f);
@@ -389,14 +423,14 @@ cudaError_t launch_any(const NormArgs& a, cudaStream_t st) {
 
 template <int DT>
 cudaError_t launch_dt(const NormArgs& a, cudaStream_t st) {
-  // odd widths, strides and groups (4096 x 4096: 88 us, the vector kernel 23 us)
+  // odd widths, strides and groups (4096 x 4096: 89 us, the vector kernel 24 us)
   if (!vec_ok(a)) return launch_any<DT>(a, st);
   // Few rows: a vector a thread, for latency; many: more loads in flight a thread
-  // (1, 2 vectors: 16 x 2048 2.2, 2.6 us, 148 x 4096 2.7, 2.9 us, 148 x 8192 3.6, 3.4 us,
-  // 4096 x 2048 14.0, 13.7 us, 4096 x 8192 46, 43 us).  A CTA of 1024 threads ends at
+  // (1, 2 vectors: 16 x 2048 2.1, 2.5 us, 148 x 4096 2.5, 2.8 us, 148 x 8192 3.4, 3.4 us,
+  // 4096 x 2048 13.9, 13.5 us, 4096 x 8192 47, 44 us).  A CTA of 1024 threads ends at
   // 16384 elements; the wider rows' eight vectors cost up to half more where both
-  // could be taken (4096 x 14336: 111, 74 us), a fifth of the other kernel's time (2048 x
-  // 32768: 118, 563 us).
+  // could be taken (4096 x 14336: 114, 76 us), a fifth of the other kernel's time (2048 x
+  // 32768: 121, 567 us).
   if (a.M <= 148 && a.K <= 4096) return launch_vec<DT, 1>(a, st);
   return a.K <= 16384 ? launch_vec<DT, 2>(a, st) : launch_vec<DT, 8>(a, st);
 }

@@ -490,12 +490,11 @@ bq_status bq_moe_combine(const void* y, int64_t ldy, const int32_t* inv_perm,
  * y is fp32 and is quantised unrounded (a separate norm and bq_quant_act
  * would round it to bf16 in between).  s is amax / Q in one IEEE division; a row's
  * 1 / sqrt is off by a few units in the last place, as the order of its sum has it,
- * and may differ by that between strides and alignments.  The codes are rounded to
- * nearest even from r * (weight + weight_offset) times Q / its largest magnitude in
- * the group, which is y / s without the row's factor: they do not depend on strides
- * or alignment, and may be either neighbour where y / s lies within fp32's error of
- * the middle between two codes.  The sum of squares is fp32: |r| up to 2^50, and for
- * eps = 0 each row's largest from 2^-50 on.
+ * and may differ by that between strides and alignments.  The codes are y / s
+ * without the row's factor: with t = r * (weight + weight_offset) in fp32, t * Q / max
+ * |t| of the group, correctly rounded, then to the nearest code, ties to even; they
+ * do not depend on strides or alignment.  The sum of squares is fp32: |r| up to
+ * 2^50, and for eps = 0 each row's largest from 2^-50 on.
  * x: bf16 [M, K] (row stride ldx >= K); residual: bf16 [M, K] (row stride ldr) or
  * NULL; weight: bf16 [K]; weight_offset: 0, or 1 for weights stored as their
  * difference from 1.  q: codes [M, K] (row stride ldq), s: fp32

@@ -463,3 +463,28 @@ def test_attention_with_a_row_bound_far_above_the_rows(L, D):                # n
     got = bq.kv_attention(q, c, off, ln, table, 2 ** 31 - 1, 300)
     bq.check_device_status()
     assert ((got.double() - want).abs() <= tol).all()
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [bq.INT8, bq.FP8_E4M3])
+@pytest.mark.parametrize("M,K,group", [(300, 4096, 128), (64, 2048, 2048), (40, 14336, 64), (20, 1000, 8)])
+def test_norm_codes_are_those_of_exact_quotients(L, M, K, group, dtype):     # noqa: F811
+    """code = t Q / max |t| to nearest, ties to even, with t = r w: a product of two bf16 is
+    exact in fp32, a quotient that is no tie lies farther from one than fp32's half step
+    (both have 16 bits: at least 2^-20 of itself), and a tie is exact in 64 bits."""
+    g = gen(M + K + group)
+    x = (randn(g, M, K) * torch.exp2(torch.arange(M, device="cuda") % 9 - 4.0)[:, None]).bfloat16()
+    w = (1 + 0.2 * randn(g, K)).bfloat16()
+    x[:, ::3] = (x[:, ::3].float() * 4).round().bfloat16()       # many quotients in the middle of two codes
+    t = x.to(F8) * w.to(F8)
+    amax = t.view(M, -1, group).abs().amax(2, keepdim=True)
+    n = torch.where(amax > 0, t.view(M, -1, group) * ref.QMAX[dtype] / torch.where(amax > 0, amax, 1.0), 0.0)
+    if dtype == bq.INT8:
+        assert ((n - n.floor()) == 0.5).sum() > 10
+        want = n.round().to(torch.int8).view(torch.uint8)
+    else:
+        want = n.float().to(ref.FP8).view(torch.uint8)
+    want = want.view(M, K)
+    for view in (x, shifted(x)):
+        q, _ = bq.rmsnorm_quant(view, w, group_k=group, dtype=dtype)
+        assert torch.equal(q, want), f"{int((q != want).sum())} of {q.numel()} codes"
