@@ -78,10 +78,11 @@ __device__ __forceinline__ float rcp(float x) {
   return y;
 }
 
-// a / b from r near 1 / b: the quotient's remainder is exact in one FMA, and the
-// quotient corrected by it is off by less than one last place (Markstein,
+// a / b from r = 1 / b, correctly rounded: the quotient's remainder is exact in one FMA,
+// and the quotient corrected by it is the correctly rounded one (Markstein,
 // "Computation of elementary functions on the IBM RISC System/6000 processor",
-// 1990).  For operands far from the ends of fp32.
+// 1990; checked for every mantissa of a with b = 127 and 448).  For operands far from
+// the ends of fp32.
 __device__ __forceinline__ float quotient(float a, float b, float r) {
   const float q = a * r;
   return fmaf(fmaf(-q, b, a), r, q);
@@ -150,9 +151,9 @@ __device__ __forceinline__ uint32_t e4m3x4(const float* t, const Factor& f) {
 
 // Scale of an INT8 or FP8 group and the factor of its codes from amax = max |t|, where
 // y = t rstd and t = r (w + w_off): rstd falls out of y / s, so the codes are those of
-// t Q / max |t|, and the scale is max |t| rstd / Q.  Both kernels go by it, so that codes do not depend on the order
-// of a row's sum, nor on strides and alignment.  False where the factor may not be a
-// number; the codes are then those of y / s, divided.
+// t Q / max |t|, and the scale is max |t| rstd / Q.  Both kernels go by it, so that codes
+// do not depend on the order of a row's sum, nor on strides and alignment.  False where
+// the factor may not be a number; the codes are then those of y / s, divided.
 template <int DT>
 __device__ __forceinline__ bool group_factor(float amax, float rstd, float& sc, Factor& f) {
   constexpr float kQ = DT == kInt8 ? 127.0f : 448.0f;
