@@ -23,7 +23,8 @@
 // scale) and mo a reference of the row, the weight is 2^(y - mo), so the product
 // with the bare codes is the value sum in units of 2^mo whatever the scales are,
 // and l += weight / vs is the softmax sum in the same units: one exponential
-// serves both (value_scale in attn_common.cuh: for which scales).  Scores, sums and O are fp32; the weights are fp16, the type of the codes they are multiplied with.
+// serves both (value_scale in attn_common.cuh: for which scales).  Scores, sums and
+// O are fp32; the weights are fp16, the type of the codes they are multiplied with.
 // mo is set 8 below the largest y, and raised (and O rescaled) only when y passes it
 // by more than 15: weights end at 2^15, fp16 at 2^16, and a rescale is rare.  So a
 // weight is off by at most half a step (2^-11 of it) if it is within 2^-22 of the
@@ -37,11 +38,12 @@
 // of the two products over the pairs that causality leaves, for some milliseconds of
 // calls one behind the other; 677 us, 812 TFLOP/s, in a run of hundreds, in which the
 // card's power limit lowers its clock.  Bound by the tensor cores as they are fed: with
-// neither softmax nor conversion in the way the products alone take 508 us, since a score product of 64 keys reads as much of Q
-// from shared memory as one of 128 would.  128 scores at a time halve that, but
-// tensor memory then holds one block a row tile, so that the products wait for the
-// softmax and the other way round (723 us).  The softmax adds 85 us, the conversion
-// 60 us; a CTA's start and end cost about two key tiles of 2.7 us.
+// neither softmax nor conversion in the way the products alone take 508 us, since a
+// score product of 64 keys reads as much of Q from shared memory as one of 128 would.
+// 128 scores at a time halve that, but tensor memory then holds one block a row tile,
+// so that the products wait for the softmax and the other way round (723 us).  The
+// softmax adds 85 us, the conversion 60 us (measured at 645 us in all); a CTA's start
+// and end cost about two key tiles of 2.7 us.
 //
 // Every wait is bounded (2 s); on expiry the CTA records a timeout in the
 // device status word, drains its MMAs, frees its tensor memory and exits.
