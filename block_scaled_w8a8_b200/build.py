@@ -96,7 +96,10 @@ def _link_ext(obj: str):
 
 def _ext_stamp() -> str:
     """What the extension fits besides its sources: the interpreter and torch."""
-    import torch
+    try:
+        import torch
+    except ImportError:
+        return ""
     return f"python {sysconfig.get_config_var('SOABI')}, torch {torch.__version__}\n"
 
 
@@ -117,7 +120,11 @@ def _build_ext():
         with open(EXT_STAMP, "w") as f:
             f.write(_ext_stamp())
     except (ImportError, OSError, RuntimeError) as e:
-        # the C ABI and the calls through ctypes do not need it; those that do raise
+        # the C ABI and the calls through ctypes do not need it; those that do raise.  An
+        # old one would call the new library with the old arguments.
+        for f in (EXT, EXT_STAMP):
+            if os.path.exists(f):
+                os.remove(f)
         warnings.warn(f"{os.path.basename(EXT)} is not built (norm, rotary positions, cache and "
                       f"attention cannot be called on torch tensors): {e}", RuntimeWarning,
                       stacklevel=3)

@@ -493,8 +493,9 @@ bq_status bq_moe_combine(const void* y, int64_t ldy, const int32_t* inv_perm,
  * and may differ by that between strides and alignments.  The codes are y / s
  * without the row's factor: with t = r * (weight + weight_offset) in fp32, t * Q / max
  * |t| of the group, correctly rounded, then to the nearest code, ties to even; they
- * do not depend on strides or alignment.  The sum of squares is fp32: |r| up to
- * 2^50, and for eps = 0 each row's largest from 2^-50 on.
+ * do not depend on strides or alignment (max |t| and max |y| of a group within 2^-100
+ * .. 2^100; beyond, the codes are those of y / s).  The sum of squares is fp32: |r|
+ * up to 2^50, and for eps = 0 each row's largest from 2^-50 on.
  * x: bf16 [M, K] (row stride ldx >= K); residual: bf16 [M, K] (row stride ldr) or
  * NULL; weight: bf16 [K]; weight_offset: 0, or 1 for weights stored as their
  * difference from 1.  q: codes [M, K] (row stride ldq), s: fp32

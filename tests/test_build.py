@@ -1,5 +1,6 @@
 """What the build does about the extension module: a missing host compiler, another torch."""
 import os
+import sys
 
 import pytest
 
@@ -39,3 +40,19 @@ def test_another_torch_builds_the_extension_anew(built, monkeypatch):
     b.build()
     b.build()
     assert len(made) == 2
+
+
+def test_without_torch_the_library_is_still_built(built, monkeypatch):
+    monkeypatch.setitem(sys.modules, "torch", None)         # importing it raises
+    with pytest.warns(RuntimeWarning, match="is not built"):
+        assert b.build() == b.LIB
+
+
+def test_an_extension_that_cannot_be_built_anew_does_not_stay(built, monkeypatch):
+    """It would call the new library with the old arguments."""
+    for f in (b.EXT, b.EXT_STAMP):
+        open(f, "w").close()
+    monkeypatch.setenv("CXX", "/nowhere/c++")
+    with pytest.warns(RuntimeWarning, match="is not built"):
+        b.build()
+    assert not os.path.exists(b.EXT) and not os.path.exists(b.EXT_STAMP)
