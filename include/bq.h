@@ -611,9 +611,10 @@ bq_status bq_kv_attention_workspace_size(int64_t B, int64_t T, int64_t Hq, int64
  * k_j, v_j = code * scale.  Scores, softmax statistics and sums are fp32, and out
  * is rounded once to bf16; the weights that multiply the value codes may be rounded
  * to fp16, by 2^-11 of themselves within 2^-22 of a row's largest softmax_j * scale,
- * by 2^-33 of that largest below.  Value scales may be 0 or lie between 2^-70 and
- * 2^30, in any mixture (0 for codes of 0; beyond, keys may be lost from the sum).  A
- * row that sees no key gives zeros and lse = -inf.
+ * by 2^-33 of that largest below.  Value scales may be 0 (for codes of 0) or lie
+ * between 2^-70 and 2^30, in any mixture: 0 counts as 2^-70 in that largest, and
+ * beyond, keys may be lost from the sum.  A row that sees no key gives zeros and
+ * lse = -inf.
  * Slots of a page behind kv_lens[b] may hold any bytes, and pages that hold only
  * keys in front of every row's window need not exist (any number in the table).
  * The keys and values that some row of a sequence sees, and its queries, must be
